@@ -60,6 +60,8 @@ enum { AH_F32 = 0, AH_BF16 = 1 };
 #define AH_MAX_DIM 16384     /* d */
 
 #define AH_MAX_ASSIGN_LEAVES 4096 /* L for ah_assign_leaves */
+#define AH_MAX_GROUPS 65536       /* L of the grouped products */
+#define AH_MAX_WIDTH (1 << 20)    /* n and k of the grouped products */
 #define AH_MAX_LEAF_BIAS (1 << 24) /* bias_bound of the residual scan */
 
 /* code_stride value selecting the tiled code layout (see ah_tile_codes); a
@@ -407,6 +409,114 @@ int ah_scan_topk_residual(const int8_t* lut_i8, int64_t nq, int32_t B, const uin
 int ah_reorder_exact(const float* q, int64_t nq, int32_t d, const void* base, int32_t base_dtype,
                      int64_t n, const int32_t* cand_ids, int32_t R, int32_t k, int32_t* ids_out,
                      float* scores_out, void* stream);
+
+/* ===========================================================================
+ * The learned query side: products and a loss for the model that makes the
+ * queries (linear layers in int8, a projection for each leaf with its
+ * gradients) and for training it against a search's answers.  Row strides are
+ * in elements; a float type is AH_F32 or AH_BF16.
+ */
+
+/* ---------------------------------------------------------------------------
+ * Int8 products with a scale for each token (row of x) and channel (row of w).
+ *
+ * ah_i8_quantize_rows: step s_i = max_j |x_ij| / 127 (float32), codes
+ * clip(rint(x_ij / s_i), -127, 127); a zero row has step 0 and codes 0, a row
+ * with a NaN or an infinity step NaN and codes 0 (its products are NaN, other
+ * rows' are not touched).  Unlike ah_sq8_quantize nothing is clipped off.
+ *   x [n] rows of d elements, x_stride >= d apart;  codes_out int8 [n][d];  scale_out float32 [n]
+ * ah_i8_matmul: out[i][j] = ((float)(x8_i . w8_j) * x_scale[i]) * w_scale[j]
+ * (+ bias[j]), the dot exact in int32, float32 products and sum in this
+ * order, rounded once to out's type.  With documents as w this is the whole
+ * plane of the scores that ah_sq8_scan_topk ranks.
+ *   x8 int8 [m][k];  w8 int8 [n][k];  bias float32 [n] or NULL;  out [m][n]
+ * ah_i8_linear: ah_i8_quantize_rows of x, then ah_i8_matmul.
+ *   workspace >= ah_i8_linear_workspace_bytes(m, k) bytes, 16-byte aligned
+ * Any k and alignment is accepted; k % 16 == 0 with 16-byte aligned x8 and w8 is the fast form.
+ * Errors: AH_ERR_SHAPE (m, n < 0, k or d < 1, x_stride < k), AH_ERR_UNSUPPORTED
+ * (a dtype, k or d > AH_MAX_DIM, m or n >= 2^31, workspace not aligned), AH_ERR_NULL,
+ * AH_ERR_WORKSPACE.  m == 0 or n == 0 is a successful no-op.
+ */
+int ah_i8_quantize_rows(const void* x, int32_t x_dtype, int64_t n, int32_t d, int64_t x_stride, int8_t* codes_out,
+                        float* scale_out, void* stream);
+int ah_i8_matmul(const int8_t* x8, const float* x_scale, int64_t m, const int8_t* w8, const float* w_scale, int64_t n,
+                 int32_t k, const float* bias, void* out, int32_t out_dtype, void* stream);
+size_t ah_i8_linear_workspace_bytes(int64_t m, int32_t k);
+int ah_i8_linear(const void* x, int32_t x_dtype, int64_t m, int32_t k, int64_t x_stride, const int8_t* w8,
+                 const float* w_scale, int64_t n, const float* bias, void* out, int32_t out_dtype, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products grouped by leaf: every leaf l has its own matrix W_l, and each query
+ * goes through the matrices of its leaves.  A slot is one (query, leaf) pair:
+ * slot s belongs to query s / fan.
+ *
+ * ah_group_rows: the slots by (leaf, slot).
+ *   leaves      int32 [n]      leaf of each slot (ah_partition_score's leaves_out,
+ *                              [nq][fan]); one outside [0, L) means no leaf
+ *   offsets_out int64 [L+1]    leaf l has the grouped rows [offsets[l], offsets[l+1])
+ *   order_out   int32 [n]      slot of each grouped row; slots without a leaf come last
+ *   workspace   >= ah_group_rows_workspace_bytes(n, L) bytes (0 up to 4,096 slots)
+ * Errors: AH_ERR_SHAPE (n < 0, L < 1), AH_ERR_UNSUPPORTED (L >
+ * AH_MAX_ASSIGN_LEAVES, n >= 2^31), AH_ERR_NULL, AH_ERR_WORKSPACE.
+ *
+ * The products.  With p a grouped row of leaf l, and s = order[p]:
+ *   ah_grouped_matmul      out[s] = W_l x[s / fan]
+ *   ah_grouped_matmul_dx   dx[i] = sum over the slots s of query i of W_l^T dy[s]
+ *   ah_grouped_matmul_dw   dW_l = sum over the rows of leaf l of dy[s] x[s / fan]^T
+ * Rows of no leaf give out[s] = 0 and add nothing; a leaf without rows has dW_l =
+ * 0.  Sums are float32 (in a fixed order: results are the same from call to
+ * call), rounded once to the output's type; dx adds its fan terms in float32
+ * before that.
+ *   x  bf16, slots / fan rows of k elements, x_stride apart;  w bf16 [L][n][k]
+ *   dy bf16, slots rows of n elements, dy_stride apart
+ *   offsets int64 [L+1] ascending (as ah_group_rows or an index's leaf_offsets)
+ *   order   int32 [slots], each slot once; or NULL (fan == 1): row p is slot p
+ *   out [slots][n], dx_out [slots / fan][k], dw_out [L][n][k], of out_dtype
+ *   workspace >= ah_grouped_dx_workspace_bytes(slots, k, fan) bytes, 16-byte aligned (0 for fan 1)
+ * Any sizes and alignment are accepted; n and k multiples of 8 with 16-byte aligned rows are the fast form.
+ * Values of offsets and order outside their ranges are never followed out of the arrays.
+ * Errors: AH_ERR_SHAPE (slots < 0, fan < 1, slots % fan, L, n or k < 1, a
+ * stride below its row, no order with fan > 1), AH_ERR_UNSUPPORTED (out_dtype, L >
+ * AH_MAX_GROUPS, n or k > AH_MAX_WIDTH, slots >= 2^31, workspace not aligned),
+ * AH_ERR_NULL, AH_ERR_WORKSPACE.  slots == 0 is a no-op (dw_out is set to 0).
+ */
+size_t ah_group_rows_workspace_bytes(int64_t n, int32_t L);
+int ah_group_rows(const int32_t* leaves, int64_t n, int32_t L, int64_t* offsets_out, int32_t* order_out,
+                  void* workspace, size_t workspace_bytes, void* stream);
+int ah_grouped_matmul(const void* x, int64_t x_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                      const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, void* out,
+                      int32_t out_dtype, void* stream);
+size_t ah_grouped_dx_workspace_bytes(int64_t slots, int32_t k, int32_t fan);
+int ah_grouped_matmul_dx(const void* dy, int64_t dy_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                         const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, void* dx_out,
+                         int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int32_t L, int32_t n,
+                         int32_t k, const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan,
+                         void* dw_out, int32_t out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Distillation from a teacher's best scores: the loss of a student that scores
+ * all V items against a list (ids, scores) as every search here returns it, and
+ * its gradient.  Per row, with p = softmax(scores / tau) over the row's entries
+ * and q = softmax(logits / tau) over all V:
+ *   loss   = tau^2 sum_j p_j (log p_j - log q[ids_j])        (float32)
+ *   grad_v = row_weight * tau (q_v - sum of p_j over the entries with ids_j = v)
+ * An entry counts if its id is in [0, V) and its score is not -inf; a row
+ * without one has loss 0 and gradient 0.  A logit of -inf has q = 0 (loss +inf
+ * if the teacher wants it); a NaN or +inf makes its own row NaN.
+ *   logits   [n] rows of V elements of dtype, stride apart;  ids int32 [n][k];  scores float32 [n][k]
+ *   row_weight float32 [n] (the gradient of the total with respect to each row's loss) or NULL = 1
+ *   loss_out float32 [n];  grad_out of dtype, rows grad_stride apart, or NULL; may be logits itself
+ *   workspace >= ah_distill_workspace_bytes(n, V) bytes, 16-byte aligned
+ * Errors: AH_ERR_SHAPE (n < 0, V, k < 1, a stride < V, tau not positive and finite),
+ * AH_ERR_UNSUPPORTED (dtype, k > AH_MAX_R, V >= 2^31, tau outside 1e-30 .. 1e30, workspace not
+ * aligned), AH_ERR_NULL, AH_ERR_WORKSPACE.
+ */
+size_t ah_distill_workspace_bytes(int64_t n, int64_t V);
+int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
+                    const float* scores, int32_t k, float tau, const float* row_weight, float* loss_out,
+                    void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -36,6 +36,10 @@ EXPORTS = (
     "ah_encode", "ah_encode_sweep", "ah_pq_update_workspace_bytes", "ah_pq_update",
     "ah_tiled_codes_bytes", "ah_tile_codes",
     "ah_reorder_exact",
+    "ah_i8_quantize_rows", "ah_i8_matmul", "ah_i8_linear_workspace_bytes", "ah_i8_linear",
+    "ah_group_rows_workspace_bytes", "ah_group_rows", "ah_grouped_matmul",
+    "ah_grouped_dx_workspace_bytes", "ah_grouped_matmul_dx", "ah_grouped_matmul_dw",
+    "ah_distill_workspace_bytes", "ah_distill_topk",
 )
 # every symbol include/ah_instrument.h declares (measurement hooks)
 INSTRUMENT_EXPORTS = ("ah_scan_topk_timed", "ah_scan_workspace_counters", "ah_hbm_read_probe")
@@ -111,6 +115,31 @@ def lib() -> C.CDLL:
         L.ah_tile_codes.argtypes = [vp, i32, i64, i32, vp, sz, vp]
         L.ah_reorder_exact.restype = C.c_int
         L.ah_reorder_exact.argtypes = [vp, i64, i32, vp, i32, i64, vp, i32, i32, vp, vp, vp]
+        f32 = C.c_float
+        L.ah_i8_quantize_rows.restype = C.c_int
+        L.ah_i8_quantize_rows.argtypes = [vp, i32, i64, i32, i64, vp, vp, vp]
+        L.ah_i8_matmul.restype = C.c_int
+        L.ah_i8_matmul.argtypes = [vp, vp, i64, vp, vp, i64, i32, vp, vp, i32, vp]
+        L.ah_i8_linear_workspace_bytes.restype = sz
+        L.ah_i8_linear_workspace_bytes.argtypes = [i64, i32]
+        L.ah_i8_linear.restype = C.c_int
+        L.ah_i8_linear.argtypes = [vp, i32, i64, i32, i64, vp, vp, i64, vp, vp, i32, vp, sz, vp]
+        L.ah_group_rows_workspace_bytes.restype = sz
+        L.ah_group_rows_workspace_bytes.argtypes = [i64, i32]
+        L.ah_group_rows.restype = C.c_int
+        L.ah_group_rows.argtypes = [vp, i64, i32, vp, vp, vp, sz, vp]
+        L.ah_grouped_matmul.restype = C.c_int
+        L.ah_grouped_matmul.argtypes = [vp, i64, vp, i32, i32, i32, vp, vp, i64, i32, vp, i32, vp]
+        L.ah_grouped_dx_workspace_bytes.restype = sz
+        L.ah_grouped_dx_workspace_bytes.argtypes = [i64, i32, i32]
+        L.ah_grouped_matmul_dx.restype = C.c_int
+        L.ah_grouped_matmul_dx.argtypes = [vp, i64, vp, i32, i32, i32, vp, vp, i64, i32, vp, i32, vp, sz, vp]
+        L.ah_grouped_matmul_dw.restype = C.c_int
+        L.ah_grouped_matmul_dw.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, vp, i64, i32, vp, i32, vp]
+        L.ah_distill_workspace_bytes.restype = sz
+        L.ah_distill_workspace_bytes.argtypes = [i64, i64]
+        L.ah_distill_topk.restype = C.c_int
+        L.ah_distill_topk.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp]
         L.ah_scan_topk_noalloc.restype = C.c_int
         L.ah_scan_topk_noalloc.argtypes = [vp, i64, i32, vp, i32, i64, vp, vp, i32, vp, i32, i32, vp, vp, vp]
         L.ah_scan_workspace_counters.restype = C.c_int
@@ -569,6 +598,239 @@ def ah_reorder_exact(q, base, cand_ids, k, ids_out=None, scores_out=None, stream
     _check(lib().ah_reorder_exact(_ptr(q), nq, d, _ptr(base), dt, n, _ptr(cand_ids), R, k, _ptr(ids_out),
                                   _ptr(scores_out), _stream(stream)), "ah_reorder_exact")
     return ids_out, scores_out
+
+
+# ----------------------------------------------------------------------------- learned query side
+_FLOATS = {torch.float32: AH_F32, torch.bfloat16: AH_BF16}
+
+
+def _float_code(dtype, name):
+    if dtype not in _FLOATS:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _FLOATS[dtype]
+
+
+def _rows(t, dtype, name):
+    """A 2-D device tensor whose rows may lie further apart than they are long; returns (tensor, stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims")
+    n, d = t.shape
+    stride = t.stride(0) if n > 1 else max(t.stride(0), d)
+    if (d > 1 and t.stride(1) != 1) or stride < d:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return t, stride
+
+
+def _empty(shape, dtype, device, stream):
+    """Device memory that belongs to the stream the call runs on (so that it is not
+    handed to other work before the call has finished)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, shape, dtype, name, device, stream):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _work(t, need, name, device, stream):
+    if t is None:
+        return _empty(need, torch.uint8, device, stream) if need else None
+    _dev(t, torch.uint8, name)
+    return t
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel()
+
+
+def ah_i8_quantize_rows(x, codes_out=None, scale_out=None, stream=None):
+    """Int8 codes and float32 steps (max |x| / 127) of the rows of x (float32 or bfloat16 [n, d])."""
+    x, xs = _rows(x, None, "x")
+    dt = _float_code(x.dtype, "x")
+    n, d = x.shape
+    codes_out = _out(codes_out, (n, d), torch.int8, "codes_out", x.device, stream)
+    scale_out = _out(scale_out, (n,), torch.float32, "scale_out", x.device, stream)
+    _check(lib().ah_i8_quantize_rows(_ptr(x), dt, n, d, xs, _ptr(codes_out), _ptr(scale_out), _stream(stream)),
+           "ah_i8_quantize_rows")
+    return codes_out, scale_out
+
+
+def _channels(w8, w_scale, bias, k):
+    _dev(w8, torch.int8, "w8", 2)
+    _dev(w_scale, torch.float32, "w_scale", 1)
+    _dev(bias, torch.float32, "bias", 1)
+    n = w8.shape[0]
+    if w8.shape[1] != k:
+        raise ValueError("w8 and x differ in their width")
+    if w_scale.numel() != n or (bias is not None and bias.numel() != n):
+        raise ValueError("w_scale and bias need one entry for each row of w8")
+    return n
+
+
+def ah_i8_matmul(x8, x_scale, w8, w_scale, bias=None, out_dtype=torch.float32, out=None, stream=None):
+    """((float)(x8 . w8) * x_scale) * w_scale (+ bias) for every row of x8 [m, k] and of w8 [n, k]."""
+    _dev(x8, torch.int8, "x8", 2)
+    _dev(x_scale, torch.float32, "x_scale", 1)
+    m, k = x8.shape
+    if x_scale.numel() != m:
+        raise ValueError("x_scale needs one entry for each row of x8")
+    n = _channels(w8, w_scale, bias, k)
+    dt = _float_code(out_dtype if out is None else out.dtype, "out")
+    out = _out(out, (m, n), out_dtype if out is None else out.dtype, "out", x8.device, stream)
+    _check(lib().ah_i8_matmul(_ptr(x8), _ptr(x_scale), m, _ptr(w8), _ptr(w_scale), n, k, _ptr(bias), _ptr(out), dt,
+                              _stream(stream)), "ah_i8_matmul")
+    return out
+
+
+def ah_i8_linear_workspace_bytes(m: int, k: int) -> int:
+    return int(lib().ah_i8_linear_workspace_bytes(m, k))
+
+
+def ah_i8_linear(x, w8, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """A linear layer in int8: the rows of x (float32 or bfloat16 [m, k]) quantised, times w8 [n, k]."""
+    x, xs = _rows(x, None, "x")
+    dt = _float_code(x.dtype, "x")
+    m, k = x.shape
+    n = _channels(w8, w_scale, bias, k)
+    odt = _float_code(out_dtype if out is None else out.dtype, "out")
+    out = _out(out, (m, n), out_dtype if out is None else out.dtype, "out", x.device, stream)
+    workspace = _work(workspace, ah_i8_linear_workspace_bytes(m, k), "workspace", x.device, stream)
+    _check(lib().ah_i8_linear(_ptr(x), dt, m, k, xs, _ptr(w8), _ptr(w_scale), n, _ptr(bias), _ptr(out), odt,
+                              _ptr(workspace), _nbytes(workspace), _stream(stream)), "ah_i8_linear")
+    return out
+
+
+def ah_group_rows_workspace_bytes(n: int, L: int) -> int:
+    return int(lib().ah_group_rows_workspace_bytes(n, L))
+
+
+def ah_group_rows(leaves, L, offsets_out=None, order_out=None, workspace=None, stream=None):
+    """Slots in leaf order: (offsets int64 [L + 1], order int32 [slots]) for leaves int32 of any
+    shape (slots in memory order; a leaf outside [0, L) means none, such slots come last)."""
+    _dev(leaves, torch.int32, "leaves")
+    n, L = leaves.numel(), int(L)
+    offsets_out = _out(offsets_out, (L + 1,), torch.int64, "offsets_out", leaves.device, stream)
+    order_out = _out(order_out, (n,), torch.int32, "order_out", leaves.device, stream)
+    workspace = _work(workspace, ah_group_rows_workspace_bytes(n, L), "workspace", leaves.device, stream)
+    _check(lib().ah_group_rows(_ptr(leaves), n, L, _ptr(offsets_out), _ptr(order_out), _ptr(workspace),
+                               _nbytes(workspace), _stream(stream)), "ah_group_rows")
+    return offsets_out, order_out
+
+
+def _groups(offsets, order, fan, slots, L):
+    _dev(offsets, torch.int64, "offsets", 1)
+    _dev(order, torch.int32, "order", 1)
+    if offsets.numel() != L + 1:
+        raise ValueError("offsets needs one entry more than there are leaves")
+    if order is not None and order.numel() != slots:
+        raise ValueError("order needs one entry for each slot")
+    if order is None and fan != 1:
+        raise ValueError("rows without an order cannot be shared (fan > 1)")
+
+
+def ah_grouped_matmul(x, w, offsets, order=None, fan=1, out_dtype=torch.bfloat16, out=None, stream=None):
+    """out[s] = W_leaf(s) x[s // fan] for every slot s: x bfloat16 [m, k], w bfloat16 [L, n, k],
+    offsets and order as from ah_group_rows; returns [m * fan, n]."""
+    x, xs = _rows(x, torch.bfloat16, "x")
+    _dev(w, torch.bfloat16, "w", 3)
+    m, k = x.shape
+    L, n, kw = w.shape
+    if kw != k:
+        raise ValueError("w and x differ in their width")
+    slots = m * fan
+    _groups(offsets, order, fan, slots, L)
+    dtype = out_dtype if out is None else out.dtype
+    odt = _float_code(dtype, "out")
+    out = _out(out, (slots, n), dtype, "out", x.device, stream)
+    _check(lib().ah_grouped_matmul(_ptr(x), xs, _ptr(w), L, n, k, _ptr(offsets), _ptr(order), slots, fan, _ptr(out),
+                                   odt, _stream(stream)), "ah_grouped_matmul")
+    return out
+
+
+def ah_grouped_dx_workspace_bytes(slots: int, k: int, fan: int) -> int:
+    return int(lib().ah_grouped_dx_workspace_bytes(slots, k, fan))
+
+
+def ah_grouped_matmul_dx(dy, w, offsets, order=None, fan=1, out_dtype=torch.bfloat16, dx_out=None, workspace=None,
+                         stream=None):
+    """Gradient of ah_grouped_matmul with respect to x: dy bfloat16 [m * fan, n] -> [m, k]."""
+    dy, dys = _rows(dy, torch.bfloat16, "dy")
+    _dev(w, torch.bfloat16, "w", 3)
+    slots, n = dy.shape
+    L, nw, k = w.shape
+    if nw != n or fan < 1 or slots % fan:
+        raise ValueError("dy needs fan rows of the width of w's output for each query")
+    _groups(offsets, order, fan, slots, L)
+    dtype = out_dtype if dx_out is None else dx_out.dtype
+    odt = _float_code(dtype, "dx_out")
+    dx_out = _out(dx_out, (slots // fan, k), dtype, "dx_out", dy.device, stream)
+    workspace = _work(workspace, ah_grouped_dx_workspace_bytes(slots, k, fan), "workspace", dy.device, stream)
+    _check(lib().ah_grouped_matmul_dx(_ptr(dy), dys, _ptr(w), L, n, k, _ptr(offsets), _ptr(order), slots, fan,
+                                      _ptr(dx_out), odt, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "ah_grouped_matmul_dx")
+    return dx_out
+
+
+def ah_grouped_matmul_dw(dy, x, offsets, order=None, fan=1, out_dtype=torch.float32, dw_out=None, stream=None):
+    """Gradient of ah_grouped_matmul with respect to w: dy bfloat16 [m * fan, n], x bfloat16 [m, k] -> [L, n, k]."""
+    dy, dys = _rows(dy, torch.bfloat16, "dy")
+    x, xs = _rows(x, torch.bfloat16, "x")
+    slots, n = dy.shape
+    m, k = x.shape
+    if slots != m * fan:
+        raise ValueError("dy needs fan rows for each row of x")
+    L = offsets.numel() - 1
+    _groups(offsets, order, fan, slots, L)
+    dtype = out_dtype if dw_out is None else dw_out.dtype
+    odt = _float_code(dtype, "dw_out")
+    dw_out = _out(dw_out, (L, n, k), dtype, "dw_out", dy.device, stream)
+    _check(lib().ah_grouped_matmul_dw(_ptr(dy), dys, _ptr(x), xs, L, n, k, _ptr(offsets), _ptr(order), slots, fan,
+                                      _ptr(dw_out), odt, _stream(stream)), "ah_grouped_matmul_dw")
+    return dw_out
+
+
+def ah_distill_workspace_bytes(n: int, V: int) -> int:
+    return int(lib().ah_distill_workspace_bytes(n, V))
+
+
+def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=True, loss_out=None, grad_out=None,
+                    workspace=None, stream=None):
+    """Loss (float32 [n]) of a student's logits (float32 or bfloat16 [n, V]) against a teacher's best
+    (ids int32, scores float32 [n, k]) and, with want_grad, its gradient times row_weight (else None)."""
+    logits, zs = _rows(logits, None, "logits")
+    dt = _float_code(logits.dtype, "logits")
+    n, V = logits.shape
+    _dev(ids, torch.int32, "ids", 2)
+    _dev(scores, torch.float32, "scores", 2)
+    if ids.shape != scores.shape or ids.shape[0] != n:
+        raise ValueError("ids and scores need one row for each row of logits and the same width")
+    _dev(row_weight, torch.float32, "row_weight", 1)
+    if row_weight is not None and row_weight.numel() != n:
+        raise ValueError("row_weight needs one entry for each row")
+    loss_out = _out(loss_out, (n,), torch.float32, "loss_out", logits.device, stream)
+    gs = V
+    if grad_out is not None:
+        grad_out, gs = _rows(grad_out, logits.dtype, "grad_out")
+        if tuple(grad_out.shape) != (n, V):
+            raise ValueError("grad_out must have the shape of logits")
+    elif want_grad:
+        grad_out = _empty((n, V), logits.dtype, logits.device, stream)
+    workspace = _work(workspace, ah_distill_workspace_bytes(n, V), "workspace", logits.device, stream)
+    _check(lib().ah_distill_topk(_ptr(logits), dt, n, V, zs, _ptr(ids), _ptr(scores), ids.shape[1], float(tau),
+                                 _ptr(row_weight), _ptr(loss_out), _ptr(grad_out), gs, _ptr(workspace),
+                                 _nbytes(workspace), _stream(stream)), "ah_distill_topk")
+    return loss_out, grad_out
 
 
 # ----------------------------------------------------------------------------- measurement hooks

@@ -371,4 +371,134 @@ int ah_reorder_exact(const float* q, int64_t nq, int32_t d, const void* base, in
                                          scores_out, static_cast<hipStream_t>(stream)));
 }
 
+static bool float_type(int32_t t) { return t == AH_F32 || t == AH_BF16; }
+
+int ah_i8_quantize_rows(const void* x, int32_t x_dtype, int64_t n, int32_t d, int64_t x_stride, int8_t* codes_out,
+                        float* scale_out, void* stream) {
+    if (n < 0 || d < 1 || x_stride < d) return AH_ERR_SHAPE;
+    if (!float_type(x_dtype) || d > AH_MAX_DIM) return AH_ERR_UNSUPPORTED;
+    if (n == 0) return AH_OK;
+    if (!x || !codes_out || !scale_out) return AH_ERR_NULL;
+    return hip_status(ah::launch_i8_quantize(x, x_dtype, n, d, x_stride, codes_out, scale_out,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int ah_i8_matmul(const int8_t* x8, const float* x_scale, int64_t m, const int8_t* w8, const float* w_scale, int64_t n,
+                 int32_t k, const float* bias, void* out, int32_t out_dtype, void* stream) {
+    if (m < 0 || n < 0 || k < 1) return AH_ERR_SHAPE;
+    if (!float_type(out_dtype) || k > AH_MAX_DIM || m >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31))
+        return AH_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return AH_OK;
+    if (!x8 || !x_scale || !w8 || !w_scale || !out) return AH_ERR_NULL;
+    return hip_status(ah::launch_i8_matmul(x8, x_scale, m, w8, w_scale, n, k, bias, out, out_dtype,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+size_t ah_i8_linear_workspace_bytes(int64_t m, int32_t k) {
+    if (m < 0 || k < 1) return 0;
+    return ah::i8_linear_workspace_bytes(m, k);
+}
+
+int ah_i8_linear(const void* x, int32_t x_dtype, int64_t m, int32_t k, int64_t x_stride, const int8_t* w8,
+                 const float* w_scale, int64_t n, const float* bias, void* out, int32_t out_dtype, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    if (m < 0 || n < 0 || k < 1 || x_stride < k) return AH_ERR_SHAPE;
+    if (!float_type(x_dtype) || !float_type(out_dtype) || k > AH_MAX_DIM || m >= ((int64_t)1 << 31) ||
+        n >= ((int64_t)1 << 31))
+        return AH_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return AH_OK;
+    if (!x || !w8 || !w_scale || !out) return AH_ERR_NULL;
+    if (!workspace || workspace_bytes < ah::i8_linear_workspace_bytes(m, k)) return AH_ERR_WORKSPACE;
+    if (!a16(workspace)) return AH_ERR_UNSUPPORTED;
+    return hip_status(ah::launch_i8_linear(x, x_dtype, m, k, x_stride, w8, w_scale, n, bias, out, out_dtype, workspace,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+size_t ah_group_rows_workspace_bytes(int64_t n, int32_t L) {
+    if (n < 0 || L < 1) return 0;
+    return ah::group_rows_workspace_bytes(n, L);
+}
+
+int ah_group_rows(const int32_t* leaves, int64_t n, int32_t L, int64_t* offsets_out, int32_t* order_out,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (n < 0 || L < 1) return AH_ERR_SHAPE;
+    if (L > AH_MAX_ASSIGN_LEAVES || n >= ((int64_t)1 << 31)) return AH_ERR_UNSUPPORTED;
+    if (!offsets_out || (n > 0 && (!leaves || !order_out))) return AH_ERR_NULL;
+    const size_t need = ah::group_rows_workspace_bytes(n, L);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return AH_ERR_WORKSPACE;
+    return hip_status(ah::launch_group_rows(leaves, n, L, offsets_out, order_out, workspace,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+// Sizes that the grouped products share (AH_OK also when there is no row).
+static int grouped_check(int64_t slots, int32_t fan, int32_t L, int32_t n, int32_t k, int64_t a_stride, int64_t a_min,
+                         int32_t out_dtype) {
+    if (slots < 0 || fan < 1 || slots % fan != 0 || L < 1 || n < 1 || k < 1 || a_stride < a_min) return AH_ERR_SHAPE;
+    if (!float_type(out_dtype) || L > AH_MAX_GROUPS || n > AH_MAX_WIDTH || k > AH_MAX_WIDTH ||
+        slots >= ((int64_t)1 << 31))
+        return AH_ERR_UNSUPPORTED;
+    return AH_OK;
+}
+
+int ah_grouped_matmul(const void* x, int64_t x_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                      const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, void* out,
+                      int32_t out_dtype, void* stream) {
+    const int chk = grouped_check(slots, fan, L, n, k, x_stride, k, out_dtype);
+    if (chk != AH_OK || slots == 0) return chk;
+    if (!order && fan != 1) return AH_ERR_SHAPE;
+    if (!x || !w || !offsets || !out) return AH_ERR_NULL;
+    const ah::GroupedProblem g{x, x_stride, nullptr, 0, w, L, n, k, offsets, order, slots, fan};
+    return hip_status(ah::launch_grouped(g, out, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t ah_grouped_dx_workspace_bytes(int64_t slots, int32_t k, int32_t fan) {
+    if (slots < 0 || k < 1 || fan < 1) return 0;
+    return ah::grouped_dx_workspace_bytes(slots, k, fan);
+}
+
+int ah_grouped_matmul_dx(const void* dy, int64_t dy_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                         const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, void* dx_out,
+                         int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    const int chk = grouped_check(slots, fan, L, n, k, dy_stride, n, out_dtype);
+    if (chk != AH_OK || slots == 0) return chk;
+    if (!order && fan != 1) return AH_ERR_SHAPE;
+    if (!dy || !w || !offsets || !dx_out) return AH_ERR_NULL;
+    const size_t need = ah::grouped_dx_workspace_bytes(slots, k, fan);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return AH_ERR_WORKSPACE;
+    if (need > 0 && !a16(workspace)) return AH_ERR_UNSUPPORTED;
+    const ah::GroupedProblem g{nullptr, 0, dy, dy_stride, w, L, n, k, offsets, order, slots, fan};
+    return hip_status(ah::launch_grouped_dx(g, dx_out, out_dtype, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, int32_t L, int32_t n,
+                         int32_t k, const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan,
+                         void* dw_out, int32_t out_dtype, void* stream) {
+    const int chk = grouped_check(slots, fan, L, n, k, dy_stride, n, out_dtype);
+    if (chk != AH_OK) return chk;
+    if (x_stride < k || (slots > 0 && !order && fan != 1)) return AH_ERR_SHAPE;
+    if ((slots > 0 && (!dy || !x)) || !offsets || !dw_out) return AH_ERR_NULL;
+    const ah::GroupedProblem g{x, x_stride, dy, dy_stride, nullptr, L, n, k, offsets, order, slots, fan};
+    return hip_status(ah::launch_grouped_dw(g, dw_out, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t ah_distill_workspace_bytes(int64_t n, int64_t V) {
+    if (n < 0 || V < 1) return 0;
+    return ah::distill_workspace_bytes(n, V);
+}
+
+int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
+                    const float* scores, int32_t k, float tau, const float* row_weight, float* loss_out,
+                    void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    if (n < 0 || V < 1 || stride < V || k < 1 || !(tau > 0.0f) || !(tau < 1e30f) || (grad_out && grad_stride < V))
+        return AH_ERR_SHAPE;
+    if (!float_type(dtype) || k > AH_MAX_R || V >= ((int64_t)1 << 31) || tau < 1e-30f) return AH_ERR_UNSUPPORTED;
+    if (n == 0) return AH_OK;
+    if (!logits || !ids || !scores || !loss_out) return AH_ERR_NULL;
+    const size_t need = ah::distill_workspace_bytes(n, V);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return AH_ERR_WORKSPACE;
+    if (need > 0 && !a16(workspace)) return AH_ERR_UNSUPPORTED;
+    return hip_status(ah::launch_distill(logits, dtype, n, V, stride, ids, scores, k, tau, row_weight, loss_out,
+                                         grad_out, grad_stride, workspace, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

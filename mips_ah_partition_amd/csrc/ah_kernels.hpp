@@ -98,4 +98,41 @@ hipError_t launch_reorder(const float* q, int64_t nq, int32_t d, const void* bas
                           int64_t n, const int32_t* cand, int32_t R, int32_t k, int32_t* ids,
                           float* scores, hipStream_t stream);
 
+// Int8 products with a scale for each token and channel.
+hipError_t launch_i8_quantize(const void* x, int32_t dtype, int64_t n, int32_t d, int64_t xs, int8_t* codes,
+                              float* scale, hipStream_t stream);
+hipError_t launch_i8_matmul(const int8_t* x8, const float* xs, int64_t m, const int8_t* w8, const float* ws, int64_t n,
+                            int32_t k, const float* bias, void* out, int32_t out_dtype, hipStream_t stream);
+size_t i8_linear_workspace_bytes(int64_t m, int32_t k);
+hipError_t launch_i8_linear(const void* x, int32_t dtype, int64_t m, int32_t k, int64_t xs, const int8_t* w8,
+                            const float* ws, int64_t n, const float* bias, void* out, int32_t out_dtype, void* work,
+                            hipStream_t stream);
+
+// Rows grouped by leaf: the order of the rows, the products and their gradients.
+size_t group_rows_workspace_bytes(int64_t n, int32_t L);
+hipError_t launch_group_rows(const int32_t* leaves, int64_t n, int32_t L, int64_t* offsets, int32_t* order, void* ws,
+                             hipStream_t stream);
+struct GroupedProblem {
+    const void* x;   // bf16 [slots / fan][x_stride]
+    int64_t x_stride;
+    const void* dy;  // bf16 [slots][dy_stride]
+    int64_t dy_stride;
+    const void* w;   // bf16 [L][n][k]
+    int32_t L, n, k;
+    const int64_t* offsets;
+    const int32_t* order;
+    int64_t slots;
+    int32_t fan;
+};
+hipError_t launch_grouped(const GroupedProblem& g, void* out, int32_t out_dtype, hipStream_t stream);
+size_t grouped_dx_workspace_bytes(int64_t slots, int32_t k, int32_t fan);
+hipError_t launch_grouped_dx(const GroupedProblem& g, void* out, int32_t out_dtype, void* ws, hipStream_t stream);
+hipError_t launch_grouped_dw(const GroupedProblem& g, void* out, int32_t out_dtype, hipStream_t stream);
+
+// Distillation from a teacher's (ids, scores): loss and gradient.
+size_t distill_workspace_bytes(int64_t n, int64_t V);
+hipError_t launch_distill(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
+                          const float* scores, int32_t k, float tau, const float* weight, float* loss, void* grad,
+                          int64_t grad_stride, void* ws, hipStream_t stream);
+
 }  // namespace ah
