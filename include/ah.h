@@ -434,7 +434,7 @@ int ah_reorder_exact(const float* q, int64_t nq, int32_t d, const void* base, in
  *   workspace >= ah_i8_linear_workspace_bytes(m, k) bytes, 16-byte aligned
  * Any k and alignment is accepted; k % 16 == 0 with 16-byte aligned x8 and w8 is the fast form.
  * Errors: AH_ERR_SHAPE (m, n < 0, k or d < 1, x_stride < k), AH_ERR_UNSUPPORTED
- * (a dtype, k or d > AH_MAX_DIM, m or n >= 2^31, workspace not aligned), AH_ERR_NULL,
+ * (a dtype, k or d > AH_MAX_DIM, m or n > 2^30, workspace not aligned), AH_ERR_NULL,
  * AH_ERR_WORKSPACE.  m == 0 or n == 0 is a successful no-op.
  */
 int ah_i8_quantize_rows(const void* x, int32_t x_dtype, int64_t n, int32_t d, int64_t x_stride, int8_t* codes_out,
@@ -478,7 +478,7 @@ int ah_i8_linear(const void* x, int32_t x_dtype, int64_t m, int32_t k, int64_t x
  * Values of offsets and order outside their ranges are never followed out of the arrays.
  * Errors: AH_ERR_SHAPE (slots < 0, fan < 1, slots % fan, L, n or k < 1, a
  * stride below its row, no order with fan > 1), AH_ERR_UNSUPPORTED (out_dtype, L >
- * AH_MAX_GROUPS, n or k > AH_MAX_WIDTH, slots >= 2^31, workspace not aligned),
+ * AH_MAX_GROUPS, n or k > AH_MAX_WIDTH, slots > 2^30, workspace not aligned),
  * AH_ERR_NULL, AH_ERR_WORKSPACE.  slots == 0 is a no-op (dw_out is set to 0).
  */
 size_t ah_group_rows_workspace_bytes(int64_t n, int32_t L);

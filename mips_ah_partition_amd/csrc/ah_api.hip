@@ -386,7 +386,7 @@ int ah_i8_quantize_rows(const void* x, int32_t x_dtype, int64_t n, int32_t d, in
 int ah_i8_matmul(const int8_t* x8, const float* x_scale, int64_t m, const int8_t* w8, const float* w_scale, int64_t n,
                  int32_t k, const float* bias, void* out, int32_t out_dtype, void* stream) {
     if (m < 0 || n < 0 || k < 1) return AH_ERR_SHAPE;
-    if (!float_type(out_dtype) || k > AH_MAX_DIM || m >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31))
+    if (!float_type(out_dtype) || k > AH_MAX_DIM || m > ((int64_t)1 << 30) || n > ((int64_t)1 << 30))
         return AH_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return AH_OK;
     if (!x8 || !x_scale || !w8 || !w_scale || !out) return AH_ERR_NULL;
@@ -403,8 +403,8 @@ int ah_i8_linear(const void* x, int32_t x_dtype, int64_t m, int32_t k, int64_t x
                  const float* w_scale, int64_t n, const float* bias, void* out, int32_t out_dtype, void* workspace,
                  size_t workspace_bytes, void* stream) {
     if (m < 0 || n < 0 || k < 1 || x_stride < k) return AH_ERR_SHAPE;
-    if (!float_type(x_dtype) || !float_type(out_dtype) || k > AH_MAX_DIM || m >= ((int64_t)1 << 31) ||
-        n >= ((int64_t)1 << 31))
+    if (!float_type(x_dtype) || !float_type(out_dtype) || k > AH_MAX_DIM || m > ((int64_t)1 << 30) ||
+        n > ((int64_t)1 << 30))
         return AH_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return AH_OK;
     if (!x || !w8 || !w_scale || !out) return AH_ERR_NULL;
@@ -435,7 +435,7 @@ static int grouped_check(int64_t slots, int32_t fan, int32_t L, int32_t n, int32
                          int32_t out_dtype) {
     if (slots < 0 || fan < 1 || slots % fan != 0 || L < 1 || n < 1 || k < 1 || a_stride < a_min) return AH_ERR_SHAPE;
     if (!float_type(out_dtype) || L > AH_MAX_GROUPS || n > AH_MAX_WIDTH || k > AH_MAX_WIDTH ||
-        slots >= ((int64_t)1 << 31))
+        slots > ((int64_t)1 << 30))
         return AH_ERR_UNSUPPORTED;
     return AH_OK;
 }

@@ -11,16 +11,15 @@
 // "By column" operands have the summed index along memory rows; their LDS tiles
 // are read with the transposing LDS load (ds_read_b64_tr_b16).
 //
-// Tiles.  One step of the sum is 128 bytes of t (128 int8 or 64 bfloat16 values),
-// and every operand's step is cut into half-tiles of 16 KB: 128 rows x 128 bytes
-// ("row" operands) or 64 memory rows x 256 bytes ("by column").  Global memory goes
-// straight to LDS (16 bytes a lane); that write is linear in the lane, so
-// the swizzle that keeps the reads free of bank conflicts is applied to the
-// source address: a row operand's 16-byte chunk c of row r lies at c ^ (r & 7), a
-// by-column operand's 32-byte granule c of memory row r at c ^ (r & 3 | (r >> 3 & 1) << 2),
-// which puts the eight rows that half a wave reads at once into eight different
-// granules.  The matrix instruction takes P as its A operand, so that a lane ends
-// with four consecutive output columns of one row.
+// Tiles.  One step of the sum is 128 bytes of t (128 int8 or 64 bfloat16 values), and
+// every operand's step is cut into blocks of 8 KB: 64 rows x 128 bytes ("row" operands)
+// or 64 memory rows x 64 columns ("by column").  Global memory goes straight to LDS (16
+// bytes a lane); that write is linear in the lane, so the swizzle that keeps the reads
+// free of bank conflicts is applied to the source address: a row operand's 16-byte
+// chunk c of row r lies at c ^ key(r), a by-column operand's 32-byte granule c of memory
+// row r at c ^ (r >> 1 & 1 | (r >> 3 & 1) << 1): the eight rows that are read at
+// once then lie in eight different places.  The matrix instruction takes P as its A operand, so
+// that a lane ends with four consecutive output columns of one row.
 #include "ah_device.hpp"
 #include "ah_kernels.hpp"
 #include "../../include/ah.h"
@@ -29,13 +28,14 @@ namespace ah {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef int v2i __attribute__((ext_vector_type(2)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef short v8s __attribute__((ext_vector_type(8)));
 
 enum { kI8 = 0, kFwd = 1, kDx = 2, kDw = 3 };
 
-constexpr int kNT = 512;         // threads: 2 wave rows x 4 wave columns
-constexpr int kHalf = 16384;     // bytes of a half-tile
-constexpr int kFQ = 4, kFP = 2;  // 16-row fragments of a half-tile that one wave reads, row and column side
+constexpr int kNT = 256;     // threads: 2 x 2 waves
+constexpr int kCUs = 256;    // compute units of an MI355X (a multiple of its 8 XCDs)
+constexpr int kBlock = 8192; // bytes of a block
 
 // Source of chunks that lie outside an operand (past its sum or its columns).
 __device__ const v4i zero_chunk = {0, 0, 0, 0};
@@ -48,94 +48,44 @@ struct ProdArgs {
     const int64_t* off;    // leaf starts [L + 1]
     const int32_t* order;  // slot of each grouped row, or NULL: the row itself
     int64_t T;             // grouped rows (int8: m)
-    int32_t L, fan;
+    int32_t L;
+    uint32_t fan_mul, fan_shift;  // s / fan = s * fan_mul >> fan_shift
     int64_t I, J;          // output rows of one matrix (dw: n; else T) and columns
     int64_t red;           // summed elements (dw: unused, the leaf's rows)
     void* out;
     int32_t out_f32;
+    int32_t bypass;        // rows of whole 64-byte sectors
     const float *sx, *sw, *bias;  // int8
 };
+
+typedef const __attribute__((address_space(3))) v4i* lds_v4i;
+typedef __attribute__((address_space(3))) v4s* lds_v4s;
+typedef __attribute__((address_space(3))) char* lds_char;
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
 }
-__device__ __forceinline__ void dma16(const char* src, char* lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 16 bytes a lane from global memory to LDS, at lds + 16 * lane.  Written out because for the
+// builtin the compiler lets every later LDS read wait for all loads in flight, which
+// would undo the prefetch; the loops below wait by themselves (land).  It has no
+// output registers, so nothing that the compiler allocates can be overwritten by it, and
+// m0, which the compiler keeps nothing in, is set in the same block.
+__device__ __forceinline__ void dma16(const char* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(lds)),
+                 "v"(src));
 }
+// Barrier at which all but the newest N of a wave's memory operations have landed and its LDS
+// reads are done.  (The builtin wait, unlike one in asm, is seen by the compiler: it
+// places no waits of its own for loads that were started before.)
 template <int N>
-__device__ __forceinline__ void wait_vm() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wg_barrier() {
+__device__ __forceinline__ void land() {
     __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// Fragments of one half-tile, both 64-byte steps: f[x][kk].  The reads wait in
-// their own block: a separate wait could be passed by a use of the registers.
-template <int F>
-__device__ __forceinline__ void read_rows(v4i (&f)[F][2], uint32_t a0, uint32_t a1) {
-    if constexpr (F == 4) {
-        asm volatile(
-            "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
-            "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
-            "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
-            "ds_read_b128 %6, %8 offset:6144\n\tds_read_b128 %7, %9 offset:6144\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(f[0][0]), "=&v"(f[0][1]), "=&v"(f[1][0]), "=&v"(f[1][1]), "=&v"(f[2][0]), "=&v"(f[2][1]),
-              "=&v"(f[3][0]), "=&v"(f[3][1])
-            : "v"(a0), "v"(a1)
-            : "memory");
-    } else {
-        asm volatile(
-            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
-            "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %5 offset:2048\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(f[0][0]), "=&v"(f[0][1]), "=&v"(f[1][0]), "=&v"(f[1][1])
-            : "v"(a0), "v"(a1)
-            : "memory");
-    }
-}
-__device__ __forceinline__ v4i join(v2i a, v2i b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3); }
-// By-column: fragment x at a[x]; its summed rows g * 8 .. g * 8 + 7 (g = lane / 16) are two transposed reads.
-template <int F>
-__device__ __forceinline__ void read_cols(v4i (&f)[F][2], const uint32_t (&a)[F]) {
-    v2i r[F][4];
-    if constexpr (F == 4) {
-        asm volatile(
-            "ds_read_b64_tr_b16 %0, %16\n\tds_read_b64_tr_b16 %1, %16 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %2, %16 offset:8192\n\tds_read_b64_tr_b16 %3, %16 offset:9216\n\t"
-            "ds_read_b64_tr_b16 %4, %17\n\tds_read_b64_tr_b16 %5, %17 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %6, %17 offset:8192\n\tds_read_b64_tr_b16 %7, %17 offset:9216\n\t"
-            "ds_read_b64_tr_b16 %8, %18\n\tds_read_b64_tr_b16 %9, %18 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %10, %18 offset:8192\n\tds_read_b64_tr_b16 %11, %18 offset:9216\n\t"
-            "ds_read_b64_tr_b16 %12, %19\n\tds_read_b64_tr_b16 %13, %19 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %14, %19 offset:8192\n\tds_read_b64_tr_b16 %15, %19 offset:9216\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]),
-              "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]),
-              "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
-            : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3])
-            : "memory");
-    } else {
-        asm volatile(
-            "ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %2, %8 offset:8192\n\tds_read_b64_tr_b16 %3, %8 offset:9216\n\t"
-            "ds_read_b64_tr_b16 %4, %9\n\tds_read_b64_tr_b16 %5, %9 offset:1024\n\t"
-            "ds_read_b64_tr_b16 %6, %9 offset:8192\n\tds_read_b64_tr_b16 %7, %9 offset:9216\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]),
-              "=&v"(r[1][2]), "=&v"(r[1][3])
-            : "v"(a[0]), "v"(a[1])
-            : "memory");
-    }
-#pragma unroll
-    for (int x = 0; x < F; ++x) {
-        f[x][0] = join(r[x][0], r[x][1]);
-        f[x][1] = join(r[x][2], r[x][3]);
-    }
 }
 
 template <int MODE>
@@ -155,6 +105,28 @@ __device__ __forceinline__ typename Acc<MODE>::type mma(v4i p, v4i q, typename A
                                                        0, 0);
 }
 
+// Element of an accumulator that is kept in the accumulation registers.  (All its uses but the
+// matrix instruction are written like this and held(): left to itself the compiler keeps the sums
+// in vector registers and moves each in and out of the accumulation registers, 8 moves an
+// instruction.)  Before the first read after matrix instructions: settle().
+template <typename T>
+__device__ __forceinline__ T acc_read(T c) {
+    T v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(c));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ void held(T& c) {
+    asm volatile("" : "+a"(c));
+}
+// The wait states between a matrix instruction and a read of its result; for acc_read, which the
+// compiler does not look into, they have to be written down.
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // 16 bytes of which the first `valid` (<= 0: none) exist; ELEM bytes an element.
 template <int ELEM>
 __device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid) {
@@ -170,6 +142,8 @@ __device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid) {
                 if (4 * w + b < valid) {
                     if constexpr (ELEM == 1) {
                         v |= (uint32_t)(uint8_t)src[4 * w + b] << (8 * b);
+                    } else if constexpr (ELEM == 4) {
+                        __builtin_memcpy(&v, src + 4 * w, 4);
                     } else {
                         uint16_t u;
                         __builtin_memcpy(&u, src + 4 * w + b, 2);
@@ -186,377 +160,656 @@ __device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid) {
 __device__ __forceinline__ uint32_t bf16_bits(float f) {  // round to nearest even; NaN stays NaN
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
 }
-// Up to four consecutive outputs, `left` of which exist, at any element alignment.
-__device__ __forceinline__ void store4(void* out, int32_t f32, int64_t at, v4f v, int64_t left) {
-    if (f32) {
-        float* o = static_cast<float*>(out) + at;
-        if (left >= 4) {
-            __builtin_memcpy(o, &v, 16);
+// One wave's 32 NQ x 32 NP results to memory; sc holds the int8 scales of the tile (its 64 NP columns'
+// scales, their biases, its 64 NQ rows' steps).  The matrix instruction leaves four columns of a
+// row in a lane, 16 rows in a wave.
+//   bfloat16  the column side's fragments are read so that two of them give a lane eight
+//             consecutive columns (PERM; not by column): a store is 16 rows x 64 bytes
+//   float32   16 rows at a time, all columns (NP = 2: half of them), are turned around in LDS, rows
+//             16 bytes further apart than they are long, and stored in that order
+// Where rows are made of whole 64-byte sectors the stores bypass the caches' reuse order: the
+// results are not read here, and kept as others they push operands out of L2 (int8 to bfloat16,
+// 8192 x 4096 x 16384: 600 us without, 529 with).  Rows at other pitches share sectors and are
+// merged in L2 (float32, 1000 x 1536 x 100003: 424 us bypassing, 270 not).
+// A value that the compiler takes as new at this place: what is computed from it is not moved out of the
+// loop over tiles, where it would hold registers that the matrix loop needs.
+__device__ __forceinline__ int here(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+template <int MODE, int OB>
+constexpr bool kPerm = OB == 2 && MODE < kDx;
+template <int NP>
+constexpr int kTurnCols = NP == 2 ? 32 : 64;
+template <int NP>
+constexpr int kTurnPitch = kTurnCols<NP> * 4 + 16;
+
+__device__ __forceinline__ void store16(char* o, v4i v, int32_t bypass) {
+    if (bypass)
+        __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(o));
+    else
+        __builtin_memcpy(o, &v, 16);
+}
+
+template <int MODE, int NQ, int NP, int OB>
+__device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>::type (&acc)[2 * NQ][2 * NP],
+                                           const float* sc, char* turn, const int32_t (&out_row)[2], int32_t leaf,
+                                           int32_t j0) {
+    constexpr int FQ = 2 * NQ, FP = 2 * NP, Y = kPerm<MODE, OB> ? 2 : 1;  // fragments behind a lane's run of columns
+    constexpr int N = 4 * Y;                                             // columns of that run
+    const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
+    const int wq = wave >> 1, wp = wave & 1;
+    const int c0 = wp * 32 * NP;  // the wave's first column in the tile
+    const int64_t first = MODE == kDw ? leaf * a.I : 0;
+    auto value = [&](int x, int y, float sx, float* v) {
+        typename Acc<MODE>::type r = acc[x][y];
+        if constexpr (NQ * NP > 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r[e] = acc_read(acc[x][y][e]);
+        }
+        if constexpr (MODE == kI8) {
+            const int c = c0 + (Y == 2 ? (y >> 1) * 32 + g * 8 + (y & 1) * 4 : y * 16 + g * 4);
+            const v4f sw = *reinterpret_cast<const v4f*>(sc + c);
+            const v4f bias = *reinterpret_cast<const v4f*>(sc + 64 * NP + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = (float)r[e] * sx * sw[e];
+                if (a.bias) v[e] += bias[e];
+            }
         } else {
-            for (int r = 0; r < left; ++r) o[r] = v[r];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = r[e];
+        }
+    };
+    if constexpr (OB == 2) {
+        const bool whole = j0 + 64 * NP <= a.J;
+#pragma unroll
+        for (int x = 0; x < FQ; ++x) {
+            const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+            float sx = 0.0f;
+            if constexpr (MODE == kI8) sx = sc[128 * NP + wq * 32 * NQ + x * 16 + li];
+            char* const o = static_cast<char*>(a.out) + ((first + row) * a.J + j0 + c0 + g * N) * 2;
+#pragma unroll
+            for (int y = 0; y < FP; y += Y) {
+                float v[N];
+#pragma unroll
+                for (int u = 0; u < Y; ++u) value(x, y + u, sx, v + 4 * u);
+                uint32_t w[N / 2];
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) w[e] = bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16;
+                const int32_t left = whole ? N : (int32_t)a.J - (j0 + c0 + g * N + y * 16);
+                if (row < 0) {
+                } else if (left >= N) {
+                    if constexpr (N == 8)
+                        store16(o + y * 32, v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]}, a.bypass);
+                    else
+                        __builtin_memcpy(o + y * 32, w, 8);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (e < left)
+                            *reinterpret_cast<uint16_t*>(o + y * 32 + e * 2) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                }
+                __builtin_amdgcn_sched_barrier(0);  // one store's registers at a time
+            }
         }
     } else {
-        uint16_t* o = static_cast<uint16_t*>(out) + at;
-        uint32_t w[2] = {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
-        if (left >= 4) {
-            __builtin_memcpy(o, w, 8);
-        } else {
-            for (int r = 0; r < left; ++r) o[r] = (uint16_t)(w[r >> 1] >> (16 * (r & 1)));
+        constexpr int TC = kTurnCols<NP>, PITCH = kTurnPitch<NP>, NC = TC / 4, YP = TC / 16;
+#pragma unroll
+        for (int x = 0; x < FQ; ++x) {
+            float sx = 0.0f;
+            if constexpr (MODE == kI8) sx = sc[128 * NP + wq * 32 * NQ + x * 16 + li];
+#pragma unroll
+            for (int ps = 0; ps < FP / YP; ++ps) {
+#pragma unroll
+                for (int yy = 0; yy < YP; ++yy) {
+                    float e[4];
+                    value(x, ps * YP + yy, sx, e);
+                    *reinterpret_cast<v4f*>(turn + li * PITCH + (yy * 4 + g) * 16) = v4f{e[0], e[1], e[2], e[3]};
+                }
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int n = 0; n < NC / 4; ++n) {
+                    const int id = n * 64 + lane, r = id / NC, c = id % NC;
+                    const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + r, 64), j = j0 + c0 + ps * TC + c * 4;
+                    const v4i v = *reinterpret_cast<const v4i*>(turn + r * PITCH + c * 16);
+                    char* const o = static_cast<char*>(a.out) + ((first + row) * a.J + j) * 4;
+                    if (row < 0) {
+                    } else if (j + 4 <= a.J) {
+                        store16(o, v, a.bypass);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e < a.J) *reinterpret_cast<int*>(o + e * 4) = v[e];
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
         }
     }
 }
 
-struct Where {
-    int32_t leaf;   // -1: rows of no leaf (their outputs are zero)
-    int32_t qt;     // row tile inside the matrix (int8, dw)
-    int64_t p0, p1; // grouped rows of this tile, forward and dx (dw: the leaf's rows)
-    int64_t tp;     // column tile
+struct Tile {
+    int32_t leaf;       // -1: rows of no leaf (their outputs are zero)
+    int32_t p0, p1;     // grouped rows: of the tile (forward, dx; int8: plain rows), of the leaf (dw)
+    int32_t i0, j0;     // first output row inside the matrix (dw) and first column
+    int32_t red, nt;    // summed elements and steps
 };
 
-// Tile of a workgroup.  Consecutive workgroups go to the eight XCDs in turn, so
-// XCD x is given the x-th eighth of the tiles (their operands then share its L2),
-// and inside it eight row tiles are walked for each column tile.
-__device__ __forceinline__ int64_t xcd_tile(int64_t total) {
-    const int64_t per = (total + 7) >> 3, i = (int64_t)blockIdx.x >> 3;
-    const int64_t t = (int64_t)(blockIdx.x & 7) * per + i;
-    return i < per && t < total ? t : -1;
-}
-__device__ __forceinline__ void walk(int64_t t, int64_t nq, int64_t np, int64_t* tq, int64_t* tp) {
+// Tiles go out in eighths: consecutive workgroups sit on the eight XCDs in turn, so XCD x is given
+// the x-th eighth (its operands then share that XCD's L2), and its workgroups take it one
+// after another; inside it eight row tiles are walked for each column tile.
+__device__ __forceinline__ void walk(int64_t t, int64_t nq, int64_t np, int32_t* tq, int32_t* tp) {
     constexpr int G = 8;
     const int64_t band = t / (G * np), r = t - band * G * np;
     const int64_t h = nq - band * G < G ? nq - band * G : G;
-    *tp = r / h;
-    *tq = band * G + r % h;
+    *tp = (int32_t)(r / h);
+    *tq = (int32_t)(band * G + r % h);
+}
+
+__device__ __forceinline__ Tile uniform(Tile t) {
+    int32_t* f = &t.leaf;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Tile) / 4); ++i) f[i] = __builtin_amdgcn_readfirstlane(f[i]);
+    return t;
 }
 
 struct LocateShared {
-    int64_t wave_sum[kNT / 64];
-    Where w;
+    int32_t wave_sum[kNT / 64];
+    Tile next[2];
 };
-__device__ __forceinline__ int64_t leaf_start(const ProdArgs& a, int32_t l) {  // inside [0, T] whatever the array holds
+__device__ __forceinline__ int32_t leaf_start(const ProdArgs& a, int32_t l) {  // inside [0, T] whatever the array holds
     const int64_t o = a.off[l];
-    return o < 0 ? 0 : o > a.T ? a.T : o;
+    return (int32_t)(o < 0 ? 0 : o > a.T ? a.T : o);
 }
 // Rows of entry e: a leaf, or (L, L + 1) the rows after the last and before the first leaf.
-__device__ __forceinline__ void entry_rows(const ProdArgs& a, int32_t e, int64_t* b, int64_t* n) {
+__device__ __forceinline__ void entry_rows(const ProdArgs& a, int32_t e, int32_t* b, int32_t* n) {
     *b = e <= a.L ? leaf_start(a, e) : 0;
-    *n = (e < a.L ? leaf_start(a, e + 1) : e == a.L ? a.T : leaf_start(a, 0)) - *b;
+    *n = (e < a.L ? leaf_start(a, e + 1) : e == a.L ? (int32_t)a.T : leaf_start(a, 0)) - *b;
     if (*n < 0) *n = 0;
-}
-// The leaf and rows of this workgroup's tile, from the leaf starts on the device:
-// a prefix sum of the leaves' row tiles, one entry or a run of them per thread.
-template <int TQ>
-__device__ bool locate(const ProdArgs& a, int64_t np, LocateShared& sh, Where* out) {
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int32_t E = a.L + 2, run = (E + kNT - 1) / kNT;
-    int64_t sum = 0;
-    for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
-        int64_t b, n;
-        entry_rows(a, e, &b, &n);
-        sum += (n + TQ - 1) / TQ;
-    }
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int64_t v = __shfl_up(incl, o, 64);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 63) sh.wave_sum[wave] = incl;
-    if (tid == 0) sh.w.leaf = -2;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < kNT / 64; ++w) {
-        const int64_t s = sh.wave_sum[w];
-        if (w < wave) incl += s;
-        total += s;
-    }
-    const int64_t t = xcd_tile(total * np);
-    if (t < 0) return false;
-    int64_t tq, tp;
-    walk(t, total, np, &tq, &tp);
-    int64_t at = incl - sum;
-    if (tq >= at && tq < incl) {
-        for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
-            int64_t b, n;
-            entry_rows(a, e, &b, &n);
-            const int64_t k = (n + TQ - 1) / TQ;
-            if (tq < at + k) {
-                sh.w.leaf = e < a.L ? e : -1;
-                sh.w.p0 = b + (tq - at) * TQ;
-                sh.w.p1 = sh.w.p0 + TQ < b + n ? sh.w.p0 + TQ : b + n;
-                sh.w.tp = tp;
-                break;
-            }
-            at += k;
-        }
-    }
-    __syncthreads();
-    *out = sh.w;
-    __syncthreads();
-    return out->leaf != -2;
 }
 
 // Slot of grouped row p, or -1 if the order holds none there.
-__device__ __forceinline__ int64_t slot_of(const ProdArgs& a, int64_t p) {
+__device__ __forceinline__ int32_t slot_of(const ProdArgs& a, int32_t p) {
     if (!a.order) return p;
-    const int64_t s = a.order[p];
+    const int32_t s = a.order[p];
     return s >= 0 && s < a.T ? s : -1;
 }
 
-// Tile of HQ x HP half-tiles.  DMA: operands are 16-byte aligned with whole chunks;
-// otherwise chunks go through registers, where a chunk's missing elements become zero.
-template <int MODE, int HQ, int HP, bool DMA>
-__global__ __launch_bounds__(kNT, HQ* HP >= 4 ? 2 : 4) void prod_tile_kernel(ProdArgs a) {
-    constexpr int ELEM = MODE == kI8 ? 1 : 2;
-    constexpr bool QCOL = MODE == kDw, PCOL = MODE >= kDx;
-    constexpr int TQ = HQ * 128, TP = HP * 128, STEP = 128 / ELEM;
-    constexpr int BUF = (HQ + HP) * kHalf;
-    __shared__ __align__(1024) char lds[2 * BUF];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wq = wave >> 2, wp = wave & 3, g = lane >> 4, li = lane & 15;
-    const int64_t np = (a.J + TP - 1) / TP;
+// The query of a slot: slot / fan by a multiplication (slots are below 2^31).
+__device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
+    return (uint32_t)(((uint64_t)s * a.fan_mul) >> a.fan_shift);
+}
 
-    Where w;
-    if constexpr (MODE == kFwd || MODE == kDx) {
-        static_assert(sizeof(LocateShared) <= sizeof(lds), "");
-        if (!locate<TQ>(a, np, *reinterpret_cast<LocateShared*>(lds), &w)) return;
-    } else {
-        const int64_t nq = (a.I + TQ - 1) / TQ;
-        const int64_t t = xcd_tile(nq * np * (MODE == kDw ? a.L : 1));
-        if (t < 0) return;
-        w.leaf = (int32_t)(t / (nq * np));
-        int64_t tq, tp;
-        walk(t - w.leaf * nq * np, nq, np, &tq, &tp);
-        w.qt = (int32_t)tq;
-        w.tp = tp;
-        if constexpr (MODE == kDw) {
-            w.p0 = leaf_start(a, w.leaf);
-            w.p1 = leaf_start(a, w.leaf + 1);
-        } else {
-            w.p0 = tq * TQ;
-            w.p1 = w.p0 + TQ < a.T ? w.p0 + TQ : a.T;
-        }
-    }
-    const int64_t j0 = w.tp * TP;
-    const int64_t red = MODE == kDw ? (w.p1 > w.p0 ? w.p1 - w.p0 : 0) : w.leaf < 0 ? 0 : a.red;
-    const int nt = (int)((red + STEP - 1) / STEP);
+// Tiles of NQ x NP blocks by a grid of resident workgroups, four waves each, a wave with a
+// quarter of the tile (32 NQ x 32 NP); OB bytes an output.  DMA: operands are 16-byte aligned with
+// whole chunks, and go straight to LDS; otherwise (2 x 2) chunks go through registers, where a
+// chunk's missing elements become zero.
+//
+// Two LDS buffers, one sum step each, and two sets of fragments, 64 bytes of the sum each:
+//   first half of step G    multiplies the step's first fragments, reads its second ones
+//   barrier                 step G + 1 has landed, nobody reads step G's buffer any more
+//   second half             multiplies the second fragments, reads the first ones of step
+//                           G + 1, starts the loads of step G + 2 into step G's buffer
+// so matrix instructions run through both halves with the LDS reads and the loads issued
+// between them.  The steps of a workgroup's tiles form one sequence, so that a tile's
+// end costs its stores and nothing else: three cursors walk it, for what is multiplied, what is
+// loaded two steps ahead, and the order (rows to gather) three steps ahead.  A tile
+// has two steps at least (further ones than its sum has are zeros).
+// 4 x 4 (256 x 256, all accumulation registers, one wave a SIMD) loads 64 KB for 512 matrix
+// instructions, 3 x 4 an eighth more and 2 x 2 (two workgroups a CU) twice that for each of
+// them; tile_shape below chooses.
+template <int MODE, int NQ, int NP, int OB, bool DMA>
+__global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(ProdArgs a) {
+    constexpr int ELEM = MODE == kI8 ? 1 : 2, FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
+    constexpr bool QCOL = MODE == kDw, PCOL = MODE >= kDx, RAGGED = MODE == kFwd || MODE == kDx;
+    constexpr bool PERM = kPerm<MODE, OB>;
+    constexpr int TQ = NQ * 64, TP = NP * 64, STEP = 128 / ELEM;
+    constexpr int BUF = NB * kBlock;
+    constexpr int QR = QCOL ? 2 : MODE == kI8 ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : 2 * NQ;
+    __shared__ __align__(1024) char lds[(DMA ? 2 : 1) * BUF];
+    __shared__ __align__(16) char turns[OB == 4 ? 4 * 16 * kTurnPitch<NP> : 16];
+    __shared__ __align__(16) float scales[MODE == kI8 ? 128 * NP + 64 * NQ : 4];
+    __shared__ LocateShared sh;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wq = wave >> 1, wp = wave & 1, g = lane >> 4, li = lane & 15;
+    const int32_t np = (int32_t)((a.J + TP - 1) / TP);
     const char* const zero = reinterpret_cast<const char*>(&zero_chunk);
 
-    // this thread's 16-byte chunks: rows 64 s + tid / 8 of a row operand's half-tile,
-    // memory rows 32 s + tid / 16 of a by-column one (s = 0, 1)
-    const int rr = tid >> 3, rc = ((tid & 7) ^ (rr & 7)) * 16;
-    const int cr = tid >> 4, cf = (cr & 3) | ((cr >> 3) & 1) << 2;
-    const int cc = ((((tid & 15) >> 1) ^ cf) << 1 | (tid & 1)) * 16;
-
-    const char* qrow[QCOL ? 1 : HQ][2];
-    const char* prow[PCOL ? 1 : HP][2];
-    const char* pbase = a.p + (MODE == kFwd || MODE == kDx ? (w.leaf < 0 ? 0 : w.leaf) * a.pg : 0);
-    if constexpr (!QCOL) {
+    // Row tiles.  Ragged: a prefix sum of the leaves' row tiles from the leaf starts on the device,
+    // one entry or a run of them per thread, kept in registers: this thread's entries have
+    // the row tiles [first, last).
+    const int32_t E = a.L + 2, run = (E + kNT - 1) / kNT;
+    int32_t first = 0, last = 0;
+    int64_t nq = MODE == kDw ? (a.I + TQ - 1) / TQ : (a.T + TQ - 1) / TQ;
+    if constexpr (RAGGED) {
+        int32_t sum = 0;
+        for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
+            int32_t b, n;
+            entry_rows(a, e, &b, &n);
+            sum += (n + TQ - 1) / TQ;
+        }
+        last = wave_inclusive_sum(sum);
+        if (lane == 63) sh.wave_sum[wave] = last;
+        __syncthreads();
+        nq = 0;
 #pragma unroll
-        for (int h = 0; h < HQ; ++h)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                int64_t r = w.p0 + h * 128 + s * 64 + rr;
-                if (r >= w.p1) r = w.p0;  // rows past the tile repeat its first; their outputs are not written
-                if constexpr (MODE != kI8) {
-                    r = slot_of(a, r);
-                    if (r < 0) r = 0;
-                    if constexpr (MODE == kFwd) r = (uint32_t)r / (uint32_t)a.fan;
+        for (int w = 0; w < kNT / 64; ++w) {
+            const int32_t s = sh.wave_sum[w];
+            if (w < wave) last += s;
+            nq += s;
+        }
+        first = last - sum;
+        nq = __builtin_amdgcn_readfirstlane((int32_t)nq);
+    }
+    // dw: a leaf's tiles cost what the leaf has rows, so every XCD takes an eighth of each leaf's tiles (of
+    // leaves with fewer than eight, whole leaves).
+    const int64_t each = nq * np, eighth = (each + 7) >> 3, total = each * (MODE == kDw ? a.L : 1);
+    const bool spread = MODE == kDw && each >= 8;
+    const int64_t per = spread ? eighth * a.L : (total + 7) >> 3;
+    const int64_t tbeg = (int64_t)(blockIdx.x & 7) * per, tend = spread || tbeg + per < total ? tbeg + per : total;
+    auto steps = [&](int32_t red) { return red <= 2 * STEP ? 2 : (red + STEP - 1) / STEP; };
+    // Publishes tile t in sh.next[k] (to be read after a barrier); past the last one, rows of nothing.
+    auto find = [&](int64_t t, int k) {
+        int32_t tq, tp;
+        if (t >= tend) {
+            if (tid == 0) sh.next[k] = Tile{-1, 0, 0, 0, 0, 0, 0x7fffffff};
+        } else if constexpr (RAGGED) {
+            walk(t, nq, np, &tq, &tp);
+            if (tq >= first && tq < last) {
+                int32_t at = first;
+                for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
+                    int32_t b, n;
+                    entry_rows(a, e, &b, &n);
+                    const int32_t c = (n + TQ - 1) / TQ;
+                    if (tq < at + c) {
+                        const int32_t p0 = b + (tq - at) * TQ, p1 = p0 + TQ < b + n ? p0 + TQ : b + n;
+                        const int32_t red = e < a.L ? (int32_t)a.red : 0;
+                        sh.next[k] = Tile{e < a.L ? e : -1, p0, p1, 0, tp * TP, red, steps(red)};
+                        break;
+                    }
+                    at += c;
                 }
-                qrow[h][s] = a.q + r * a.qs;
             }
-    }
-    if constexpr (!PCOL) {
-#pragma unroll
-        for (int h = 0; h < HP; ++h)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                int64_t r = j0 + h * 128 + s * 64 + rr;
-                if (r >= a.J) r = j0;
-                prow[h][s] = pbase + r * a.ps;
+        } else if (tid == 0) {
+            int32_t leaf = 0;
+            int64_t in = t;
+            if constexpr (MODE == kDw) {
+                leaf = (int32_t)(spread ? (t - tbeg) / eighth : t / each);
+                in = spread ? (blockIdx.x & 7) * eighth + (t - tbeg) % eighth : t % each;
             }
-    }
-
-    // Chunk s of half-tile h at sum step t: its address, and in *valid the bytes of it that exist.
-    const int64_t rend = red * ELEM;
-    auto q_src = [&](int t, int h, int s, int64_t* valid) -> const char* {
-        if constexpr (!QCOL) {
-            const int64_t o = (int64_t)t * 128 + rc;
-            *valid = rend - o;
-            return qrow[h][s] + o;
-        } else {
-            const int64_t o = (int64_t)w.qt * (TQ * 2) + h * 256 + cc;
-            const int64_t p = w.p0 + (int64_t)t * STEP + s * 32 + cr;
-            const int64_t r = p < w.p1 ? slot_of(a, p) : -1;
-            *valid = r < 0 ? 0 : a.I * 2 - o;
-            return a.q + r * a.qs + o;
+            walk(in, nq, np, &tq, &tp);
+            if constexpr (MODE == kDw) {
+                const int32_t p0 = leaf_start(a, leaf), p1 = leaf_start(a, leaf + 1);
+                const int32_t red = p1 > p0 && in < each ? p1 - p0 : 0;
+                if (in >= each) tq = (int32_t)nq;  // where eighths do not come out even: past the last row
+                sh.next[k] = Tile{leaf, p0, p1, tq * TQ, tp * TP, red, steps(red)};
+            } else {
+                const int32_t p0 = tq * TQ, p1 = p0 + TQ < a.T ? p0 + TQ : (int32_t)a.T;
+                sh.next[k] = Tile{0, p0, p1, 0, tp * TP, (int32_t)a.red, steps((int32_t)a.red)};
+            }
         }
     };
-    auto p_src = [&](int t, int h, int s, int64_t* valid) -> const char* {
+
+    // This thread's 16-byte chunks, two of each block: rows 32 s + rr (of a row operand) or memory rows
+    // 32 s + rr (by column), at byte rc or cc of the row.
+    auto key = [](int r) { return (r & 3) | (((r >> 2) ^ (r >> 3)) & 1) << 2; };
+    auto ckey = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 1) << 1; };
+    const int rr = tid >> 3, rc = ((tid & 7) ^ key(rr)) * 16;
+    const int cc = ((((tid & 7) >> 1) ^ ckey(rr)) << 1 | (tid & 1)) * 16;
+
+    Tile w;                               // the tile that is loaded
+    const char* qrow[QR];                 // row operand: its rows; by column: this step's memory rows
+    const char* prow[MODE == kDw ? 2 : 1];
+    uint32_t poff[PCOL ? 1 : 2 * NP];     // rows that follow one another: offsets from prow[0], qrow[0]
+    uint32_t qoff[MODE == kI8 ? 2 * NQ : 1];
+    int32_t slot[SLOTS];                  // slots of a tile's rows; dw: of the next step's memory rows
+
+    // dw: the memory rows of step u of tile n come from the order (load_slots), and are turned into
+    // addresses when the step's loads start (set_rows).
+    auto load_slots = [&](const Tile& n, int u, int32_t(&to)[SLOTS]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int32_t r = u * STEP + s * 32 + rr, in = r < n.red ? n.p0 + r : n.p0 < a.T ? n.p0 : 0;
+            const int32_t v = a.order ? a.order[in] : in;
+            to[s] = r < n.red && v < a.T ? v : -1;
+        }
+    };
+    auto set_rows = [&](const int32_t(&from)[SLOTS]) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            qrow[s] = from[s] < 0 ? nullptr : a.q + (int64_t)from[s] * a.qs + (int64_t)w.i0 * 2 + cc;
+            prow[s] = a.p + (int64_t)query_of(a, (uint32_t)from[s]) * a.ps + (int64_t)w.j0 * 2 + cc;
+        }
+    };
+    // A tile's rows: first what has to be read (slots, output rows: lane's and 64 + lane's of this wave's
+    // part, -1: not written), later the addresses.
+    auto take_rows = [&](const Tile& n, int32_t(&rows)[2]) {
+        const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7, rr = tid >> 3;
+        if constexpr (RAGGED) {
+#pragma unroll
+            for (int s = 0; s < 2 * NQ; ++s) {
+                const int32_t r = n.p0 + s * 32 + rr;
+                slot[s] = slot_of(a, r < n.p1 ? r : n.p0 < a.T ? n.p0 : 0);  // rows past the tile repeat its first
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int32_t i = wq * 32 * NQ + u * 64 + lane;
+            if constexpr (MODE == kDw)
+                rows[u] = n.i0 + i < a.I ? n.i0 + i : -1;
+            else if constexpr (MODE == kI8)
+                rows[u] = n.p0 + i < n.p1 ? n.p0 + i : -1;
+            else
+                rows[u] = n.p0 + i < n.p1 ? slot_of(a, n.p0 + i) : -1;
+        }
+    };
+    auto set_addresses = [&]() {
+        const int rr = here(tid) >> 3;
+        if constexpr (MODE == kI8) {
+            qrow[0] = a.q + w.p0 * a.qs + rc;
+#pragma unroll
+            for (int s = 0; s < 2 * NQ; ++s) {
+                const int r = s * 32 + rr;
+                qoff[s] = w.p0 + r < w.p1 ? (uint32_t)(r * a.qs) : 0u;
+            }
+        } else if constexpr (!QCOL) {
+#pragma unroll
+            for (int s = 0; s < 2 * NQ; ++s) {
+                int32_t r = slot[s] < 0 ? 0 : slot[s];
+                if constexpr (MODE == kFwd) r = (int32_t)query_of(a, (uint32_t)r);
+                qrow[s] = a.q + (int64_t)r * a.qs + rc;
+            }
+        }
+        const char* pbase = a.p + (RAGGED && w.leaf > 0 ? w.leaf * a.pg : 0);
         if constexpr (!PCOL) {
-            const int64_t o = (int64_t)t * 128 + rc;
-            *valid = rend - o;
-            return prow[h][s] + o;
+            prow[0] = pbase + w.j0 * a.ps + rc;
+#pragma unroll
+            for (int s = 0; s < 2 * NP; ++s) {
+                const int r = s * 32 + rr;
+                poff[s] = w.j0 + r < a.J ? (uint32_t)(r * a.ps) : 0u;
+            }
         } else if constexpr (MODE == kDx) {
-            const int64_t o = j0 * 2 + h * 256 + cc, r = (int64_t)t * STEP + s * 32 + cr;
-            *valid = r < red ? a.J * 2 - o : 0;
-            return pbase + r * a.ps + o;
+            prow[0] = pbase + rr * a.ps + (int64_t)w.j0 * 2 + cc;
+        }
+    };
+    // Chunk c of a step (of block c / 2, the column side's first): its address, and how many
+    // bytes of it exist (<= 0: none).
+    auto source = [&](int u, int c, int32_t* valid) -> const char* {
+        const int s = c & 1;
+        if (c < 2 * NP) {
+            const int h = c >> 1;
+            if constexpr (!PCOL) {
+                *valid = w.red * ELEM - (u * 128 + rc);
+                return prow[0] + poff[c] + u * 128;
+            } else if constexpr (MODE == kDx) {
+                const int r = u * STEP + s * 32;
+                *valid = r + rr < w.red ? ((int32_t)a.J - w.j0) * 2 - (h * 128 + cc) : 0;
+                return prow[0] + r * a.ps + h * 128;
+            } else {
+                *valid = qrow[s] ? ((int32_t)a.J - w.j0) * 2 - (h * 128 + cc) : 0;
+                return prow[s] + h * 128;
+            }
         } else {
-            const int64_t o = j0 * 2 + h * 256 + cc;
-            const int64_t p = w.p0 + (int64_t)t * STEP + s * 32 + cr;
-            const int64_t r = p < w.p1 ? slot_of(a, p) : -1;
-            *valid = r < 0 ? 0 : a.J * 2 - o;
-            return a.p + (int64_t)((uint32_t)r / (uint32_t)a.fan) * a.ps + o;
+            const int h = (c >> 1) - NP;
+            if constexpr (!QCOL) {
+                *valid = w.red * ELEM - (u * 128 + rc);
+                if constexpr (MODE == kI8)
+                    return qrow[0] + qoff[c - 2 * NP] + u * 128;
+                else
+                    return qrow[c - 2 * NP] + u * 128;
+            } else {
+                *valid = qrow[s] ? ((int32_t)a.I - w.i0) * 2 - (h * 128 + cc) : 0;
+                return qrow[s] + h * 128;
+            }
         }
     };
 
-    // fragment addresses inside a buffer (column side first, then row side)
+    // Fragments: 16 rows (or columns) x 64 bytes of the sum, in the operand layout of the matrix
+    // instruction: lane 16 g + i holds bytes 16 g .. 16 g + 15 of row i.  By column that is eight
+    // summed rows, two transposed reads of four.
     const uint32_t base = lds_addr(lds);
-    uint32_t pa[PCOL ? kFP : 2], qa[QCOL ? kFQ : 2];
-    const int fi = (li >> 2) | (g & 1) << 2;
+    // PERM: row 4 a + b of column fragment y is column 32 (y / 2) + 8 a + 4 (y & 1) + b of the part, so
+    // that fragments 2 z and 2 z + 1 leave eight consecutive columns in a lane.
+    const int pl = PERM ? (li >> 2) * 8 + (li & 3) : li;
+    auto row_start = [&](int r, int kk) -> uint32_t { return r * 128 + (((kk * 4 + g) ^ key(r)) * 16); };
+    const uint32_t pstart[2] = {base + row_start(wp * 32 * NP + pl, 0), base + row_start(wp * 32 * NP + pl, 1)};
+    const uint32_t qstart[2] = {base + NP * kBlock + row_start(wq * 32 * NQ + li, 0),
+                                base + NP * kBlock + row_start(wq * 32 * NQ + li, 1)};
+    // by column: fragment n of an operand is granule n & 3 of block n >> 2
+    const int tr = g * 8 + (li >> 2);
+    auto col_start = [&](int n) -> uint32_t {
+        return (n >> 2) * kBlock + tr * 128 + (((n & 3) ^ ckey(tr)) * 32) + (li & 3) * 8;
+    };
+    uint32_t pcol[PCOL ? FP : 1], qcol[QCOL ? FQ : 1];
     if constexpr (PCOL) {
 #pragma unroll
-        for (int x = 0; x < kFP; ++x) pa[x] = base + (g * 8 + (li >> 2)) * 256 + ((wp * kFP + x) ^ fi) * 32 + (li & 3) * 8;
-    } else {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) pa[kk] = base + (wp * kFP * 16 + li) * 128 + (((kk * 4 + g) ^ (li & 7)) * 16);
+        for (int x = 0; x < FP; ++x) pcol[x] = base + col_start(wp * FP + x);
     }
     if constexpr (QCOL) {
 #pragma unroll
-        for (int x = 0; x < kFQ; ++x)
-            qa[x] = base + HP * kHalf + (g * 8 + (li >> 2)) * 256 + ((wq * kFQ + x) ^ fi) * 32 + (li & 3) * 8;
-    } else {
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-            qa[kk] = base + HP * kHalf + (wq * kFQ * 16 + li) * 128 + (((kk * 4 + g) ^ (li & 7)) * 16);
+        for (int x = 0; x < FQ; ++x) qcol[x] = base + NP * kBlock + col_start(wq * FQ + x);
     }
+    auto by_row = [&](uint32_t at, uint32_t o) -> v4i { return *(lds_v4i)((lds_char)(uintptr_t)at + o); };
+    auto by_col = [&](uint32_t at, uint32_t o) -> v4i {
+        const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)((lds_char)(uintptr_t)at + o));
+        const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s)((lds_char)(uintptr_t)at + o + 512));
+        return __builtin_bit_cast(v4i, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto read_p = [&](int x, int kk, uint32_t buf) -> v4i {
+        if constexpr (PCOL)
+            return by_col(pcol[x] + buf, kk * 4096);
+        else if constexpr (PERM)  // four rows on, the key's high bit changes: the other start
+            return by_row(pstart[kk ^ (x & 1)] + buf, (x >> 1) * 4096 + (x & 1) * 512);
+        else
+            return by_row(pstart[kk] + buf, x * 2048);
+    };
+    auto read_q = [&](int x, int kk, uint32_t buf) -> v4i {
+        if constexpr (QCOL)
+            return by_col(qcol[x] + buf, kk * 4096);
+        else
+            return by_row(qstart[kk] + buf, x * 2048);
+    };
 
     typedef typename Acc<MODE>::type acc_t;
-    acc_t acc[HQ][HP][kFQ][kFP];
-#pragma unroll
-    for (int x = 0; x < HQ * HP * kFQ * kFP; ++x) (&acc[0][0][0][0])[x] = acc_t{0, 0, 0, 0};
-
-    v4i stage[DMA ? 1 : 2 * (HQ + HP)];
-    auto fetch = [&](int t, int buf) {
-        char* l = lds + buf * BUF + wave * 1024;
-#pragma unroll
-        for (int h = 0; h < HP + HQ; ++h)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                int64_t valid;
-                const char* src = h < HP ? p_src(t, h, s, &valid) : q_src(t, h - HP, s, &valid);
-                if constexpr (DMA)
-                    dma16(valid > 0 ? src : zero, l + h * kHalf + s * 8192);
-                else
-                    stage[2 * h + s] = load_chunk<ELEM>(src, valid);
-            }
+    acc_t acc[FQ][FP];
+    v4i pf[2][FP], qf[2][FQ];
+    auto load = [&](int u, int c, uint32_t buf) {
+        int32_t valid;
+        const char* src = source(u, c, &valid);
+        dma16(valid > 0 ? src : zero, base + buf + c * 4096 + wave * 1024);
     };
-    auto compute = [&](int buf) {
-        const uint32_t b = buf * BUF;
-        v4i pf[HP][kFP][2], qf[kFQ][2];
+    // One half-step: the matrix instructions of fragment set kk; between them the reads of
+    // the other set from `buf` and (kk = 1) the loads of step u into the other buffer.
+    auto half_step = [&](int kk, uint32_t buf, int u) {
+        constexpr int N = FQ + FP;  // groups: fragments to read, chunks to load
 #pragma unroll
-        for (int h = 0; h < HP; ++h) {
-            if constexpr (PCOL) {
-                uint32_t ad[kFP];
+        for (int n = 0; n < N; ++n) {
+            if (n < FQ)
+                qf[kk ^ 1][n] = read_q(n, kk ^ 1, buf);
+            else
+                pf[kk ^ 1][n - FQ] = read_p(n - FQ, kk ^ 1, buf);
+            if (kk == 1) load(u, n, BUF - buf);
 #pragma unroll
-                for (int x = 0; x < kFP; ++x) ad[x] = pa[x] + b + h * kHalf;
-                read_cols<kFP>(pf[h], ad);
-            } else {
-                read_rows<kFP>(pf[h], pa[0] + b + h * kHalf, pa[1] + b + h * kHalf);
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < HQ; ++h) {
-            if constexpr (QCOL) {
-                uint32_t ad[kFQ];
-#pragma unroll
-                for (int x = 0; x < kFQ; ++x) ad[x] = qa[x] + b + h * kHalf;
-                read_cols<kFQ>(qf, ad);
-            } else {
-                read_rows<kFQ>(qf, qa[0] + b + h * kHalf, qa[1] + b + h * kHalf);
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                for (int hp = 0; hp < HP; ++hp)
-#pragma unroll
-                    for (int x = 0; x < kFQ; ++x)
-#pragma unroll
-                        for (int y = 0; y < kFP; ++y)
-                            acc[h][hp][x][y] = mma<MODE>(pf[hp][y][kk], qf[x][kk], acc[h][hp][x][y]);
+            for (int m = n * FQ * FP / N; m < (n + 1) * FQ * FP / N; ++m)
+                acc[m / FP][m % FP] = mma<MODE>(pf[kk][m % FP], qf[kk][m / FP], acc[m / FP][m % FP]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
+    auto clear = [&]() {
+#pragma unroll
+        for (int x = 0; x < FQ * FP; ++x) {
+            (&acc[0][0])[x] = acc_t{0, 0, 0, 0};
+            if constexpr (NQ * NP > 4) held((&acc[0][0])[x]);
+        }
+    };
+    // int8 scales of tile n: one column and one row of the tile per thread.
+    auto load_scales = [&](const Tile& n, float(&v)[3]) {
+        const int tid = here(threadIdx.x);
+        const int32_t j = n.j0 + tid < a.J ? n.j0 + tid : (int32_t)a.J - 1, r = n.p0 + tid < n.p1 ? n.p0 + tid : n.p0;
+        v[0] = a.sw[j];
+        v[1] = a.bias ? a.bias[j] : 0.0f;
+        v[2] = a.sx[r];
+    };
+    auto keep_scales = [&](const float(&v)[3]) {
+        const int tid = here(threadIdx.x);
+        if (tid < 64 * NP) {
+            scales[tid] = v[0];
+            scales[64 * NP + tid] = v[1];
+        }
+        if (tid < 64 * NQ) scales[128 * NP + tid] = v[2];
+    };
 
+    char* const turn = turns + (OB == 4 ? wave * 16 * kTurnPitch<NP> : 0);
+
+    int64_t t = tbeg + (blockIdx.x >> 3);
+    const int64_t hop = gridDim.x >> 3;
+    if (t >= tend) return;
+    find(t, 0);
+    __syncthreads();
     if constexpr (DMA) {
-        if (nt > 0) fetch(0, 0);
-        for (int t = 0; t < nt; ++t) {
-            wait_vm<0>();  // step t has landed, and every wave is done with the other buffer
-            wg_barrier();
-            if (t + 1 < nt) fetch(t + 1, (t + 1) & 1);
-            compute(t & 1);
+        Tile ws = uniform(sh.next[0]);  // the order's cursor: tile, its step, its rows
+        int32_t us = 0, rows_s[2];
+        int64_t ts = t;
+        int k = 1;
+        take_rows(ws, rows_s);
+        find(ts += hop, k);
+        int32_t slot1[SLOTS];
+        if constexpr (MODE == kDw) {
+            load_slots(ws, 0, slot);
+            load_slots(ws, 1, slot1);
         }
+        auto advance_order = [&]() {
+            if (++us == ws.nt) {
+                ws = uniform(sh.next[k]);
+                us = 0;
+                k ^= 1;
+                find(ts += hop, k);
+                take_rows(ws, rows_s);
+            }
+            if constexpr (MODE == kDw) load_slots(ws, us, slot);
+        };
+        land<0>();
+        w = ws;
+        int32_t ul = 0, rows_l[2];  // the loads' cursor
+#pragma unroll
+        for (int u = 0; u < 2; ++u) rows_l[u] = rows_s[u];
+        set_addresses();
+#pragma unroll
+        for (; ul < 2; ++ul) {
+            if constexpr (MODE == kDw) {
+                if (ul == 0)
+                    set_rows(slot);
+                else
+                    set_rows(slot1);
+            }
+#pragma unroll
+            for (int c = 0; c < 2 * NB; ++c) load(ul, c, ul * BUF);
+        }
+        us = 1;
+        advance_order();
+        Tile wc = w;  // what is multiplied
+        int32_t uc = 0, rows_c[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) rows_c[u] = rows_l[u];
+        clear();
+        land<2 * NB>();
+#pragma unroll
+        for (int x = 0; x < FQ; ++x) qf[0][x] = read_q(x, 0, 0);
+#pragma unroll
+        for (int x = 0; x < FP; ++x) pf[0][x] = read_p(x, 0, 0);
+        for (uint32_t cur = 0;; cur = BUF - cur) {
+            float sv[3] = {};
+            if constexpr (MODE == kI8) {
+                if (uc == 0) load_scales(wc, sv);
+            }
+            half_step(0, cur, 0);
+            land<0>();
+            if constexpr (MODE == kI8) {
+                if (uc == 0) keep_scales(sv);
+            }
+            if (ul == w.nt) {
+                w = ws;
+                ul = 0;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) rows_l[u] = rows_s[u];
+                set_addresses();
+            }
+            if constexpr (MODE == kDw) set_rows(slot);
+            advance_order();
+            half_step(1, BUF - cur, ul++);
+            if (++uc < wc.nt) continue;
+            if constexpr (NQ * NP > 4) settle();
+            store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows_c, wc.leaf, wc.j0);
+            t += hop;
+            if (t >= tend) break;
+            wc = w;
+            uc = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) rows_c[u] = rows_l[u];
+            clear();
+        }
+        land<0>();  // no load is left in flight towards LDS
     } else {
-        if (nt > 0) fetch(0, 0);
-        for (int t = 0; t < nt; ++t) {
-            __syncthreads();
+        int32_t rows[2];
+        v4i stage[2 * NB];
+        auto fetch = [&](int u) {
+            if constexpr (MODE == kDw) {
+                load_slots(w, u, slot);
+                set_rows(slot);
+            }
 #pragma unroll
-            for (int h = 0; h < HP + HQ; ++h)
+            for (int c = 0; c < 2 * NB; ++c) {
+                int32_t valid;
+                const char* src = source(u, c, &valid);
+                stage[c] = load_chunk<ELEM>(src, valid);
+            }
+        };
+        for (;;) {
+            w = uniform(sh.next[0]);
+            if constexpr (MODE == kI8) {
+                float sv[3];
+                load_scales(w, sv);
+                keep_scales(sv);
+            }
+            take_rows(w, rows);
+            set_addresses();
+            clear();
+            fetch(0);
+            for (int u = 0; u < w.nt; ++u) {
+                __syncthreads();
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    *reinterpret_cast<v4i*>(lds + h * kHalf + s * 8192 + tid * 16) = stage[2 * h + s];
+                for (int c = 0; c < 2 * NB; ++c) *reinterpret_cast<v4i*>(lds + c * 4096 + tid * 16) = stage[c];
+                __syncthreads();
+                if (u + 1 < w.nt) fetch(u + 1);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                    for (int x = 0; x < FQ; ++x) qf[kk][x] = read_q(x, kk, 0);
+#pragma unroll
+                    for (int x = 0; x < FP; ++x) pf[kk][x] = read_p(x, kk, 0);
+#pragma unroll
+                    for (int m = 0; m < FQ * FP; ++m)
+                        acc[m / FP][m % FP] = mma<MODE>(pf[kk][m % FP], qf[kk][m / FP], acc[m / FP][m % FP]);
+                }
+            }
+            store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows, w.leaf, w.j0);
+            t += hop;
+            if (t >= tend) break;
             __syncthreads();
-            if (t + 1 < nt) fetch(t + 1, 0);
-            compute(0);
+            find(t, 0);
+            __syncthreads();
         }
     }
-
-#pragma unroll
-    for (int h = 0; h < HQ; ++h)
-#pragma unroll
-        for (int x = 0; x < kFQ; ++x) {
-            const int i = h * 128 + wq * 64 + x * 16 + li;
-            int64_t row;
-            float sx = 0.0f;
-            if constexpr (MODE == kDw) {
-                row = (int64_t)w.qt * TQ + i;
-                if (row >= a.I) continue;
-                row += w.leaf * a.I;
-            } else {
-                row = w.p0 + i;
-                if (row >= w.p1) continue;
-                if constexpr (MODE == kI8) {
-                    sx = a.sx[row];
-                } else {
-                    row = slot_of(a, row);
-                    if (row < 0) continue;
-                }
-            }
-#pragma unroll
-            for (int hp = 0; hp < HP; ++hp)
-#pragma unroll
-                for (int y = 0; y < kFP; ++y) {
-                    const int64_t j = j0 + hp * 128 + wp * 32 + y * 16 + g * 4;
-                    if (j >= a.J) continue;
-                    v4f v;
-                    if constexpr (MODE == kI8) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int64_t jr = j + r < a.J ? j + r : a.J - 1;
-                            v[r] = (float)acc[h][hp][x][y][r] * sx * a.sw[jr];
-                            if (a.bias) v[r] += a.bias[jr];
-                        }
-                    } else {
-                        v = acc[h][hp][x][y];
-                    }
-                    store4(a.out, a.out_f32, row * a.J + j, v, a.J - j);
-                }
-        }
 }
 
-// Tokens to int8 codes: step = max |x| / 127 (float32), code = rint(x / step).
-// One workgroup per row; a row with a NaN or an infinity gets step NaN and zero
-// codes, so that it spoils its own outputs and no others.
+// Tokens to int8 codes: step = max |x| / 127 (float32), code = rint(x / step), the division IEEE.
+// A row with a NaN or an infinity gets step NaN and zero codes, so that it spoils its own
+// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out): a workgroup per row, which is
+// read once and kept in registers up to 8,192 elements, in chunks of 16 bytes at any alignment.
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
     if constexpr (sizeof(T) == 4)
@@ -564,47 +817,93 @@ __device__ __forceinline__ float to_f32(T v) {
     else
         return __uint_as_float((uint32_t)v << 16);
 }
+constexpr int kQuantKeep = 4;  // chunks a thread keeps
 template <typename T>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const T* x, int64_t n, int32_t d, int64_t xs, int8_t* codes,
                                                           float* scale) {
+    constexpr int NV = 16 / sizeof(T);
     __shared__ float red[4];
+    const int tid = threadIdx.x;
+    const int32_t chunks = (d + NV - 1) / NV;
     for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
         const T* xr = x + row * xs;
+        auto fetch = [&](int32_t c) -> v4i {
+            return load_chunk<sizeof(T)>(reinterpret_cast<const char*>(xr + (int64_t)c * NV),
+                                         ((int64_t)d - (int64_t)c * NV) * (int64_t)sizeof(T));
+        };
+        v4i keep[kQuantKeep];
         float m = 0.0f;
-        for (int32_t j = threadIdx.x; j < d; j += 256) {
-            const float v = fabsf(to_f32(xr[j]));
-            m = v < INFINITY ? fmaxf(m, v) : NAN;
-            if (!(v < INFINITY)) break;
-        }
-        bool bad = !(m < INFINITY);
-        m = bad ? 0.0f : m;
+        bool bad = false;
+        auto look = [&](v4i v) {
+            T e[NV];
+            __builtin_memcpy(e, &v, 16);
+#pragma unroll
+            for (int r = 0; r < NV; ++r) {
+                const float f = fabsf(to_f32(e[r]));
+                bad |= !(f < INFINITY);
+                m = fmaxf(m, f);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kQuantKeep; ++k)
+            if (tid + k * 256 < chunks) keep[k] = fetch(tid + k * 256);
+#pragma unroll
+        for (int k = 0; k < kQuantKeep; ++k)
+            if (tid + k * 256 < chunks) look(keep[k]);
+        for (int32_t c = tid + kQuantKeep * 256; c < chunks; c += 256) look(fetch(c));
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        const int any = __syncthreads_or(bad);
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-        __syncthreads();
+        if ((tid & 63) == 0) red[tid >> 6] = m;
+        const int any = __syncthreads_or(bad);  // also publishes red
         const float s = any ? NAN : fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / 127.0f;
-        if (threadIdx.x == 0) scale[row] = s;
-        for (int32_t j = threadIdx.x; j < d; j += 256) {
-            const float q = s > 0.0f ? rintf(to_f32(xr[j]) / s) : 0.0f;
-            codes[row * d + j] = (int8_t)(int)fminf(fmaxf(q, -127.0f), 127.0f);
-        }
+        if (tid == 0) scale[row] = s;
+        auto write = [&](int32_t c, v4i v) {
+            T e[NV];
+            int8_t q[NV];
+            __builtin_memcpy(e, &v, 16);
+#pragma unroll
+            for (int r = 0; r < NV; ++r)
+                q[r] = s > 0.0f ? (int8_t)(int)fminf(fmaxf(rintf(to_f32(e[r]) / s), -127.0f), 127.0f) : (int8_t)0;
+            int8_t* o = codes + row * d + (int64_t)c * NV;
+            if ((int64_t)(c + 1) * NV <= d) {
+                __builtin_memcpy(o, q, NV);
+            } else {
+#pragma unroll
+                for (int r = 0; r < NV; ++r)
+                    if (c * NV + r < d) o[r] = q[r];
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kQuantKeep; ++k)
+            if (tid + k * 256 < chunks) write(tid + k * 256, keep[k]);
+        for (int32_t c = tid + kQuantKeep * 256; c < chunks; c += 256) write(c, fetch(c));
         __syncthreads();
     }
 }
 
-// Sum of each row's `fan` float32 partial gradients, rounded once.
+// Sum of each row's `fan` float32 partial gradients, rounded once.  HBM-bound; four columns a thread
+// (cols % 4 == 0: the partial rows are 16-byte aligned; else one).
+template <int N>
 __global__ __launch_bounds__(256) void fan_sum_kernel(const float* part, int64_t rows, int32_t fan, int64_t cols,
                                                       void* out, int32_t out_f32) {
-    const int64_t total = rows * cols;
+    const int64_t per = cols / N, total = rows * per;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / cols, c = i - r * cols;
-        float s = 0.0f;
-        for (int32_t f = 0; f < fan; ++f) s += part[(r * fan + f) * cols + c];
-        if (out_f32)
-            static_cast<float*>(out)[i] = s;
-        else
-            static_cast<uint16_t*>(out)[i] = (uint16_t)bf16_bits(s);
+        const int64_t r = i / per, c = (i - r * per) * N;
+        float s[N] = {};
+        for (int32_t f = 0; f < fan; ++f) {
+            float v[N];
+            __builtin_memcpy(v, part + (r * fan + f) * cols + c, 4 * N);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[e] += v[e];
+        }
+        if (out_f32) {
+            __builtin_memcpy(static_cast<float*>(out) + r * cols + c, s, 4 * N);
+        } else {
+            uint16_t b[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) b[e] = (uint16_t)bf16_bits(s[e]);
+            __builtin_memcpy(static_cast<uint16_t*>(out) + r * cols + c, b, 2 * N);
+        }
     }
 }
 
@@ -612,25 +911,52 @@ inline bool chunked(const void* p, int64_t stride_bytes, int64_t width_bytes) {
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)stride_bytes | (uintptr_t)width_bytes) & 15) == 0;
 }
 
-template <int MODE, bool DMA>
+// Row tiles of TQ rows (ragged: their number is known on the device only; `most` bounds it, the
+// estimate takes every leaf to end inside a tile).
+template <int MODE>
+int64_t row_tiles(const ProdArgs& a, int64_t TQ, bool most) {
+    if (MODE == kDw) return (a.I + TQ - 1) / TQ * a.L;
+    if (MODE == kI8) return (a.T + TQ - 1) / TQ;
+    return a.T / TQ + (most ? a.L + 2 : (a.T < a.L ? a.T : a.L) / 2 + 1);
+}
+
+// Blocks of the tile's row side: 4 (of 4 x 4), 3 (of 3 x 4) or 2 (of 2 x 2).  The time is taken as the
+// rounds that the resident workgroups go through times a round's blocks a CU, over the shape's
+// rate on large products (1, 0.97 and 0.85: 32,768 rows of 64 leaves, 1536 -> 4096: 560, 582 and
+// 650 us, where rounds and ragged ends explain the first ratio).  dw always takes 2 x 2: its tiles are as
+// unequal as the leaves (16 leaves of 450 to 1,900 rows, 1536 x 1536, with dx: 302 us; 3 x 4 by a
+// workgroup for each tile 314, by resident workgroups 334).
+template <int MODE>
+int tile_shape(const ProdArgs& a) {
+    auto time = [&](int64_t TQ, int64_t TP, int64_t resident, double round) {
+        return (double)((row_tiles<MODE>(a, TQ, false) * ((a.J + TP - 1) / TP) + resident - 1) / resident) * round;
+    };
+    const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / 0.97),
+                 t2 = time(128, 128, 2 * kCUs, 8 / 0.85);
+    return t2 <= t3 && t2 <= t4 ? 2 : t3 < t4 ? 3 : 4;
+}
+
+template <int MODE, int NQ, int NP, bool DMA>
 hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
-    constexpr int HQ = 1, HP = 1;
-    const int64_t np = (a.J + HP * 128 - 1) / (HP * 128);
-    int64_t nq;
-    if (MODE == kDw)
-        nq = (a.I + HQ * 128 - 1) / (HQ * 128) * a.L;
-    else if (MODE == kI8)
-        nq = (a.T + HQ * 128 - 1) / (HQ * 128);
+    constexpr int TQ = NQ * 64, TP = NP * 64;
+    const int64_t np = (a.J + TP - 1) / TP, each = row_tiles<MODE>(a, TQ, true) * np;
+    const int64_t resident = kCUs * (NQ * NP > 4 ? 1 : 2);
+    int64_t wgs = (each + 7) / 8 * 8;
+    if (MODE == kDw) {  // a workgroup for each tile: they are of unequal length, and start as others end
+        const int64_t leaf = (a.I + TQ - 1) / TQ * np;
+        if (leaf >= 8) wgs = (leaf + 7) / 8 * 8 * a.L;
+    }
+    if ((MODE != kDw || wgs >= ((int64_t)1 << 31)) && wgs > resident) wgs = resident;
+    const dim3 grid((uint32_t)wgs);
+    if (a.out_f32)
+        hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 4, DMA>), grid, dim3(kNT), 0, stream, a);
     else
-        nq = a.T / (HQ * 128) + a.L + 2;
-    const int64_t wgs = (nq * np + 7) / 8 * 8;
-    if (wgs >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((prod_tile_kernel<MODE, HQ, HP, DMA>), dim3((uint32_t)wgs), dim3(kNT), 0, stream, a);
+        hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 2, DMA>), grid, dim3(kNT), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int MODE>
-hipError_t launch_prod(const ProdArgs& a, hipStream_t stream) {
+hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     const int e = MODE == kI8 ? 1 : 2;
     bool whole;
     if (MODE == kDw)
@@ -639,7 +965,23 @@ hipError_t launch_prod(const ProdArgs& a, hipStream_t stream) {
         whole = chunked(a.q, a.qs, a.red * e) && chunked(a.p, a.ps, a.J * e);
     else
         whole = chunked(a.q, a.qs, a.red * e) && chunked(a.p, a.ps, 0);
-    return whole ? launch_tiles<MODE, true>(a, stream) : launch_tiles<MODE, false>(a, stream);
+    // ceil(2^(31 + l) / fan) with l = ceil(log2 fan) divides every slot below 2^31 exactly
+    int l = 0;
+    while (((int64_t)1 << l) < fan) ++l;
+    a.fan_shift = 31 + l;
+    a.fan_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + fan - 1) / fan);
+    const int64_t pitch = a.J * (a.out_f32 ? 4 : 2);
+    a.bypass = MODE != kFwd && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
+    if (!whole) return launch_tiles<MODE, 2, 2, false>(a, stream);
+    if constexpr (MODE == kDw) {
+        return launch_tiles<MODE, 2, 2, true>(a, stream);
+    } else {
+        switch (tile_shape<MODE>(a)) {
+            case 4: return launch_tiles<MODE, 4, 4, true>(a, stream);
+            case 3: return launch_tiles<MODE, 3, 4, true>(a, stream);
+            default: return launch_tiles<MODE, 2, 2, true>(a, stream);
+        }
+    }
 }
 
 }  // namespace
@@ -670,7 +1012,7 @@ hipError_t launch_i8_matmul(const int8_t* x8, const float* xs, int64_t m, const 
     a.sx = xs;
     a.sw = ws;
     a.bias = bias;
-    return launch_prod<kI8>(a, stream);
+    return launch_prod<kI8>(a, 1, stream);
 }
 
 // Workspace: the tokens' codes (rows of k bytes, the block rounded up to 16) and their steps.
@@ -698,12 +1040,11 @@ hipError_t launch_grouped(const GroupedProblem& g, void* out, int32_t out_dtype,
     a.order = g.order;
     a.T = a.I = g.slots;
     a.L = g.L;
-    a.fan = g.fan;
     a.J = g.n;
     a.red = g.k;
     a.out = out;
     a.out_f32 = out_dtype == AH_F32;
-    return launch_prod<kFwd>(a, stream);
+    return launch_prod<kFwd>(a, g.fan, stream);
 }
 
 size_t grouped_dx_workspace_bytes(int64_t slots, int32_t k, int32_t fan) {
@@ -721,16 +1062,21 @@ hipError_t launch_grouped_dx(const GroupedProblem& g, void* out, int32_t out_dty
     a.order = g.order;
     a.T = a.I = g.slots;
     a.L = g.L;
-    a.fan = g.fan;
     a.J = g.k;
     a.red = g.n;
     a.out = g.fan > 1 ? ws : out;
     a.out_f32 = g.fan > 1 || out_dtype == AH_F32;
-    hipError_t e = launch_prod<kDx>(a, stream);
+    hipError_t e = launch_prod<kDx>(a, g.fan, stream);
     if (e != hipSuccess || g.fan == 1) return e;
-    const int64_t rows = g.slots / g.fan, wgs = (rows * g.k + 255) / 256;
-    hipLaunchKernelGGL(fan_sum_kernel, dim3((uint32_t)(wgs < 8192 ? wgs : 8192)), dim3(256), 0, stream,
-                       static_cast<const float*>(ws), rows, g.fan, (int64_t)g.k, out, out_dtype == AH_F32);
+    const int64_t rows = g.slots / g.fan, n = g.k % 4 == 0 ? 4 : 1, wgs = (rows * g.k / n + 255) / 256;
+    const dim3 grid((uint32_t)(wgs < 16384 ? wgs : 16384));
+    const float* part = static_cast<const float*>(ws);
+    if (n == 4)
+        hipLaunchKernelGGL(fan_sum_kernel<4>, grid, dim3(256), 0, stream, part, rows, g.fan, (int64_t)g.k, out,
+                           out_dtype == AH_F32);
+    else
+        hipLaunchKernelGGL(fan_sum_kernel<1>, grid, dim3(256), 0, stream, part, rows, g.fan, (int64_t)g.k, out,
+                           out_dtype == AH_F32);
     return hipGetLastError();
 }
 
@@ -741,15 +1087,14 @@ hipError_t launch_grouped_dw(const GroupedProblem& g, void* out, int32_t out_dty
     a.p = static_cast<const char*>(g.x);
     a.ps = g.x_stride * 2;
     a.off = g.offsets;
-    a.order = g.order;
+    a.order = g.slots > 0 ? g.order : nullptr;
     a.T = g.slots;
     a.I = g.n;
     a.L = g.L;
-    a.fan = g.fan;
     a.J = g.k;
     a.out = out;
     a.out_f32 = out_dtype == AH_F32;
-    return launch_prod<kDw>(a, stream);
+    return launch_prod<kDw>(a, g.fan, stream);
 }
 
 }  // namespace ah

@@ -85,7 +85,7 @@ def _i8_ref(torch, c, s, w, ws, bias, dtype):
 
 I8_SIZES = [(1, 1, 1), (1, 16, 4096), (1, 1536, 100), (2, 17, 33), (5, 100, 16), (16, 64, 64), (17, 128, 130),
             (33, 144, 257), (64, 4096, 70), (65, 1001, 403), (128, 256, 128), (200, 80, 515), (300, 512, 1),
-            (129, 16384, 48), (513, 272, 300), (1030, 640, 520)]
+            (129, 16384, 48), (513, 272, 300), (1030, 640, 520), (2100, 272, 7001), (3333, 1104, 4000)]
 
 
 @pytest.mark.parametrize("m,k,n", I8_SIZES)
@@ -201,7 +201,7 @@ def _close(got, ref, mag, terms, dtype_bits):
 GROUPED_SIZES = [  # rows, fan, leaves, k, n
     (1, 1, 1, 8, 8), (1, 3, 5, 64, 64), (4, 2, 300, 128, 72), (16, 4, 64, 256, 128), (33, 3, 7, 100, 77),
     (40, 1, 3, 1, 1), (150, 2, 2, 136, 264), (257, 1, 1, 520, 129), (100, 3, 9, 65, 48), (500, 4, 11, 192, 192),
-    (700, 2, 600, 40, 24), (1500, 2, 5, 320, 328)]
+    (700, 2, 600, 40, 24), (1500, 2, 5, 320, 328), (3000, 2, 6, 264, 1288), (4000, 2, 10, 1104, 1096)]
 
 
 def _grouped_case(torch, rows, fan, L, k, n, seed=0):
