@@ -604,10 +604,30 @@ def ah_reorder_exact(q, base, cand_ids, k, ids_out=None, scores_out=None, stream
 _FLOATS = {torch.float32: AH_F32, torch.bfloat16: AH_BF16}
 
 
+def _at(t):
+    """Address for a pointer argument (the argument types are declared, so a plain int will do)."""
+    return None if t is None else t.data_ptr()
+
+
+def _on(stream, t):
+    """The raw stream of a call: the one given, or the current one of t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _is(t, dtype, name, ndim):
+    """_dev in one test; what fails it is named by _dev."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a device tensor")
+        _dev(t, dtype, name, ndim)
+    return t
+
+
 def _float_code(dtype, name):
-    if dtype not in _FLOATS:
+    code = _FLOATS.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
-    return _FLOATS[dtype]
+    return code
 
 
 def _rows(t, dtype, name):
@@ -661,15 +681,16 @@ def ah_i8_quantize_rows(x, codes_out=None, scale_out=None, stream=None):
     n, d = x.shape
     codes_out = _out(codes_out, (n, d), torch.int8, "codes_out", x.device, stream)
     scale_out = _out(scale_out, (n,), torch.float32, "scale_out", x.device, stream)
-    _check(lib().ah_i8_quantize_rows(_ptr(x), dt, n, d, xs, _ptr(codes_out), _ptr(scale_out), _stream(stream)),
+    _check(lib().ah_i8_quantize_rows(_at(x), dt, n, d, xs, _at(codes_out), _at(scale_out), _on(stream, x)),
            "ah_i8_quantize_rows")
     return codes_out, scale_out
 
 
 def _channels(w8, w_scale, bias, k):
-    _dev(w8, torch.int8, "w8", 2)
-    _dev(w_scale, torch.float32, "w_scale", 1)
-    _dev(bias, torch.float32, "bias", 1)
+    _is(w8, torch.int8, "w8", 2)
+    _is(w_scale, torch.float32, "w_scale", 1)
+    if bias is not None:
+        _is(bias, torch.float32, "bias", 1)
     n = w8.shape[0]
     if w8.shape[1] != k:
         raise ValueError("w8 and x differ in their width")
@@ -680,16 +701,16 @@ def _channels(w8, w_scale, bias, k):
 
 def ah_i8_matmul(x8, x_scale, w8, w_scale, bias=None, out_dtype=torch.float32, out=None, stream=None):
     """((float)(x8 . w8) * x_scale) * w_scale (+ bias) for every row of x8 [m, k] and of w8 [n, k]."""
-    _dev(x8, torch.int8, "x8", 2)
-    _dev(x_scale, torch.float32, "x_scale", 1)
+    _is(x8, torch.int8, "x8", 2)
+    _is(x_scale, torch.float32, "x_scale", 1)
     m, k = x8.shape
     if x_scale.numel() != m:
         raise ValueError("x_scale needs one entry for each row of x8")
     n = _channels(w8, w_scale, bias, k)
     dt = _float_code(out_dtype if out is None else out.dtype, "out")
     out = _out(out, (m, n), out_dtype if out is None else out.dtype, "out", x8.device, stream)
-    _check(lib().ah_i8_matmul(_ptr(x8), _ptr(x_scale), m, _ptr(w8), _ptr(w_scale), n, k, _ptr(bias), _ptr(out), dt,
-                              _stream(stream)), "ah_i8_matmul")
+    _check(lib().ah_i8_matmul(_at(x8), _at(x_scale), m, _at(w8), _at(w_scale), n, k, _at(bias), _at(out), dt,
+                              _on(stream, x8)), "ah_i8_matmul")
     return out
 
 
@@ -706,8 +727,8 @@ def ah_i8_linear(x, w8, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, 
     odt = _float_code(out_dtype if out is None else out.dtype, "out")
     out = _out(out, (m, n), out_dtype if out is None else out.dtype, "out", x.device, stream)
     workspace = _work(workspace, ah_i8_linear_workspace_bytes(m, k), "workspace", x.device, stream)
-    _check(lib().ah_i8_linear(_ptr(x), dt, m, k, xs, _ptr(w8), _ptr(w_scale), n, _ptr(bias), _ptr(out), odt,
-                              _ptr(workspace), _nbytes(workspace), _stream(stream)), "ah_i8_linear")
+    _check(lib().ah_i8_linear(_at(x), dt, m, k, xs, _at(w8), _at(w_scale), n, _at(bias), _at(out), odt,
+                              _at(workspace), _nbytes(workspace), _on(stream, x)), "ah_i8_linear")
     return out
 
 
@@ -723,14 +744,15 @@ def ah_group_rows(leaves, L, offsets_out=None, order_out=None, workspace=None, s
     offsets_out = _out(offsets_out, (L + 1,), torch.int64, "offsets_out", leaves.device, stream)
     order_out = _out(order_out, (n,), torch.int32, "order_out", leaves.device, stream)
     workspace = _work(workspace, ah_group_rows_workspace_bytes(n, L), "workspace", leaves.device, stream)
-    _check(lib().ah_group_rows(_ptr(leaves), n, L, _ptr(offsets_out), _ptr(order_out), _ptr(workspace),
-                               _nbytes(workspace), _stream(stream)), "ah_group_rows")
+    _check(lib().ah_group_rows(_at(leaves), n, L, _at(offsets_out), _at(order_out), _at(workspace),
+                               _nbytes(workspace), _on(stream, leaves)), "ah_group_rows")
     return offsets_out, order_out
 
 
 def _groups(offsets, order, fan, slots, L):
-    _dev(offsets, torch.int64, "offsets", 1)
-    _dev(order, torch.int32, "order", 1)
+    _is(offsets, torch.int64, "offsets", 1)
+    if order is not None:
+        _is(order, torch.int32, "order", 1)
     if offsets.numel() != L + 1:
         raise ValueError("offsets needs one entry more than there are leaves")
     if order is not None and order.numel() != slots:
@@ -743,7 +765,7 @@ def ah_grouped_matmul(x, w, offsets, order=None, fan=1, out_dtype=torch.bfloat16
     """out[s] = W_leaf(s) x[s // fan] for every slot s: x bfloat16 [m, k], w bfloat16 [L, n, k],
     offsets and order as from ah_group_rows; returns [m * fan, n]."""
     x, xs = _rows(x, torch.bfloat16, "x")
-    _dev(w, torch.bfloat16, "w", 3)
+    _is(w, torch.bfloat16, "w", 3)
     m, k = x.shape
     L, n, kw = w.shape
     if kw != k:
@@ -753,8 +775,8 @@ def ah_grouped_matmul(x, w, offsets, order=None, fan=1, out_dtype=torch.bfloat16
     dtype = out_dtype if out is None else out.dtype
     odt = _float_code(dtype, "out")
     out = _out(out, (slots, n), dtype, "out", x.device, stream)
-    _check(lib().ah_grouped_matmul(_ptr(x), xs, _ptr(w), L, n, k, _ptr(offsets), _ptr(order), slots, fan, _ptr(out),
-                                   odt, _stream(stream)), "ah_grouped_matmul")
+    _check(lib().ah_grouped_matmul(_at(x), xs, _at(w), L, n, k, _at(offsets), _at(order), slots, fan, _at(out),
+                                   odt, _on(stream, x)), "ah_grouped_matmul")
     return out
 
 
@@ -766,7 +788,7 @@ def ah_grouped_matmul_dx(dy, w, offsets, order=None, fan=1, out_dtype=torch.bflo
                          stream=None):
     """Gradient of ah_grouped_matmul with respect to x: dy bfloat16 [m * fan, n] -> [m, k]."""
     dy, dys = _rows(dy, torch.bfloat16, "dy")
-    _dev(w, torch.bfloat16, "w", 3)
+    _is(w, torch.bfloat16, "w", 3)
     slots, n = dy.shape
     L, nw, k = w.shape
     if nw != n or fan < 1 or slots % fan:
@@ -776,8 +798,8 @@ def ah_grouped_matmul_dx(dy, w, offsets, order=None, fan=1, out_dtype=torch.bflo
     odt = _float_code(dtype, "dx_out")
     dx_out = _out(dx_out, (slots // fan, k), dtype, "dx_out", dy.device, stream)
     workspace = _work(workspace, ah_grouped_dx_workspace_bytes(slots, k, fan), "workspace", dy.device, stream)
-    _check(lib().ah_grouped_matmul_dx(_ptr(dy), dys, _ptr(w), L, n, k, _ptr(offsets), _ptr(order), slots, fan,
-                                      _ptr(dx_out), odt, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    _check(lib().ah_grouped_matmul_dx(_at(dy), dys, _at(w), L, n, k, _at(offsets), _at(order), slots, fan,
+                                      _at(dx_out), odt, _at(workspace), _nbytes(workspace), _on(stream, dy)),
            "ah_grouped_matmul_dx")
     return dx_out
 
@@ -795,8 +817,8 @@ def ah_grouped_matmul_dw(dy, x, offsets, order=None, fan=1, out_dtype=torch.floa
     dtype = out_dtype if dw_out is None else dw_out.dtype
     odt = _float_code(dtype, "dw_out")
     dw_out = _out(dw_out, (L, n, k), dtype, "dw_out", dy.device, stream)
-    _check(lib().ah_grouped_matmul_dw(_ptr(dy), dys, _ptr(x), xs, L, n, k, _ptr(offsets), _ptr(order), slots, fan,
-                                      _ptr(dw_out), odt, _stream(stream)), "ah_grouped_matmul_dw")
+    _check(lib().ah_grouped_matmul_dw(_at(dy), dys, _at(x), xs, L, n, k, _at(offsets), _at(order), slots, fan,
+                                      _at(dw_out), odt, _on(stream, dy)), "ah_grouped_matmul_dw")
     return dw_out
 
 
@@ -811,12 +833,11 @@ def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=Tru
     logits, zs = _rows(logits, None, "logits")
     dt = _float_code(logits.dtype, "logits")
     n, V = logits.shape
-    _dev(ids, torch.int32, "ids", 2)
-    _dev(scores, torch.float32, "scores", 2)
+    _is(ids, torch.int32, "ids", 2)
+    _is(scores, torch.float32, "scores", 2)
     if ids.shape != scores.shape or ids.shape[0] != n:
         raise ValueError("ids and scores need one row for each row of logits and the same width")
-    _dev(row_weight, torch.float32, "row_weight", 1)
-    if row_weight is not None and row_weight.numel() != n:
+    if row_weight is not None and _is(row_weight, torch.float32, "row_weight", 1).numel() != n:
         raise ValueError("row_weight needs one entry for each row")
     loss_out = _out(loss_out, (n,), torch.float32, "loss_out", logits.device, stream)
     gs = V
@@ -827,9 +848,9 @@ def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=Tru
     elif want_grad:
         grad_out = _empty((n, V), logits.dtype, logits.device, stream)
     workspace = _work(workspace, ah_distill_workspace_bytes(n, V), "workspace", logits.device, stream)
-    _check(lib().ah_distill_topk(_ptr(logits), dt, n, V, zs, _ptr(ids), _ptr(scores), ids.shape[1], float(tau),
-                                 _ptr(row_weight), _ptr(loss_out), _ptr(grad_out), gs, _ptr(workspace),
-                                 _nbytes(workspace), _stream(stream)), "ah_distill_topk")
+    _check(lib().ah_distill_topk(_at(logits), dt, n, V, zs, _at(ids), _at(scores), ids.shape[1], float(tau),
+                                 _at(row_weight), _at(loss_out), _at(grad_out), gs, _at(workspace),
+                                 _nbytes(workspace), _on(stream, logits)), "ah_distill_topk")
     return loss_out, grad_out
 
 

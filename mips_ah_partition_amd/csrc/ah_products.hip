@@ -127,31 +127,34 @@ __device__ __forceinline__ void settle() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// 16 bytes of which the first `valid` (<= 0: none) exist; ELEM bytes an element.
+// The 16 bytes v moved down by `cut` bytes (< 16), zeros above.
+__device__ __forceinline__ v4i shift_down(v4i v, int cut) {
+    const uint64_t lo = (uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32,
+                   hi = (uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
+    const int n = 8 * (cut & 7);
+    const uint64_t a = cut & 8 ? hi : lo, b = cut & 8 ? 0 : hi;
+    const uint64_t l = a >> n | (b << 1) << (63 - n), h = b >> n;
+    return v4i{(int)(uint32_t)l, (int)(uint32_t)(l >> 32), (int)(uint32_t)h, (int)(uint32_t)(h >> 32)};
+}
+// 16 bytes of a row of which the first `valid` exist (<= 0: none), `before` bytes into the row; ELEM
+// bytes an element.  A row's short end is read as the 16 bytes up to it, moved down; element by
+// element only in rows of less than 16 bytes.
 template <int ELEM>
-__device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid) {
+__device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid, int64_t before) {
     v4i r = {0, 0, 0, 0};
-    if (valid >= 16) {
-        __builtin_memcpy(&r, src, 16);
-    } else if (valid > 0) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int b = 0; b < 4; b += ELEM) {
-                if (4 * w + b < valid) {
-                    if constexpr (ELEM == 1) {
-                        v |= (uint32_t)(uint8_t)src[4 * w + b] << (8 * b);
-                    } else if constexpr (ELEM == 4) {
-                        __builtin_memcpy(&v, src + 4 * w, 4);
-                    } else {
-                        uint16_t u;
-                        __builtin_memcpy(&u, src + 4 * w + b, 2);
-                        v |= (uint32_t)u << (8 * b);
-                    }
-                }
-            }
-            r[w] = (int)v;
+    if (valid <= 0) return r;
+    const int cut = valid >= 16 ? 0 : 16 - (int)valid;
+    if (before >= cut) {
+        __builtin_memcpy(&r, src - cut, 16);
+        if (cut > 0) r = shift_down(r, cut);
+    } else {
+        for (int b = 0; b < (int)valid; b += ELEM) {  // the last element comes down to the bottom
+            uint32_t e = 0;
+            __builtin_memcpy(&e, src + (int)valid - ELEM - b, ELEM);
+            uint64_t lo = (uint32_t)r[0] | (uint64_t)(uint32_t)r[1] << 32, hi = (uint32_t)r[2] | (uint64_t)(uint32_t)r[3] << 32;
+            hi = hi << (8 * ELEM) | lo >> (64 - 8 * ELEM);
+            lo = lo << (8 * ELEM) | e;
+            r = v4i{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
         }
     }
     return r;
@@ -185,6 +188,21 @@ constexpr int kTurnCols = NP == 2 ? 32 : 64;
 template <int NP>
 constexpr int kTurnPitch = kTurnCols<NP> * 4 + 16;
 
+// The first `left` (0 < left < n) of n elements of OB bytes, in pieces of 8, 4 and 2 bytes: element by element
+// the epilogues' code would outgrow the instruction cache.
+template <int OB>
+__device__ __forceinline__ void store_left(char* o, v4i v, int32_t left) {
+    const int32_t bytes = left * OB;
+    const bool up = bytes & 8;
+    if (up) __builtin_memcpy(o, &v, 8);
+    const int a = up ? v[2] : v[0], b = up ? v[3] : v[1];
+    o += bytes & 8;
+    if (bytes & 4) __builtin_memcpy(o, &a, 4);
+    if constexpr (OB == 2) {
+        const uint16_t c = (uint16_t)(bytes & 4 ? b : a);
+        if (bytes & 2) __builtin_memcpy(o + (bytes & 4), &c, 2);
+    }
+}
 __device__ __forceinline__ void store16(char* o, v4i v, int32_t bypass) {
     if (bypass)
         __builtin_nontemporal_store(v, reinterpret_cast<v4i*>(o));
@@ -245,11 +263,9 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
                         store16(o + y * 32, v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]}, a.bypass);
                     else
                         __builtin_memcpy(o + y * 32, w, 8);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (e < left)
-                            *reinterpret_cast<uint16_t*>(o + y * 32 + e * 2) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                } else if (left > 0) {
+                    store_left<2>(o + y * 32, v4i{(int)w[0], (int)w[1], N == 8 ? (int)w[N / 2 - 2] : 0,
+                                                  N == 8 ? (int)w[N / 2 - 1] : 0}, left);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // one store's registers at a time
             }
@@ -279,10 +295,8 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
                     if (row < 0) {
                     } else if (j + 4 <= a.J) {
                         store16(o, v, a.bypass);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < a.J) *reinterpret_cast<int*>(o + e * 4) = v[e];
+                    } else if (j < a.J) {
+                        store_left<4>(o, v, (int32_t)a.J - j);
                     }
                 }
                 __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -536,12 +550,14 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             prow[0] = pbase + rr * a.ps + (int64_t)w.j0 * 2 + cc;
         }
     };
-    // Chunk c of a step (of block c / 2, the column side's first): its address, and how many
-    // bytes of it exist (<= 0: none).
-    auto source = [&](int u, int c, int32_t* valid) -> const char* {
+    // Chunk c of a step (of block c / 2, the column side's first): its address, how many bytes of it
+    // exist (<= 0: none) and how many of its memory row lie before it.
+    auto source = [&](int u, int c, int32_t* valid, int64_t* before) -> const char* {
         const int s = c & 1;
+        *before = u * 128 + rc;  // of a row operand
         if (c < 2 * NP) {
             const int h = c >> 1;
+            if constexpr (PCOL) *before = (int64_t)w.j0 * 2 + h * 128 + cc;
             if constexpr (!PCOL) {
                 *valid = w.red * ELEM - (u * 128 + rc);
                 return prow[0] + poff[c] + u * 128;
@@ -555,6 +571,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
         } else {
             const int h = (c >> 1) - NP;
+            if constexpr (QCOL) *before = (int64_t)w.i0 * 2 + h * 128 + cc;
             if constexpr (!QCOL) {
                 *valid = w.red * ELEM - (u * 128 + rc);
                 if constexpr (MODE == kI8)
@@ -619,7 +636,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     v4i pf[2][FP], qf[2][FQ];
     auto load = [&](int u, int c, uint32_t buf) {
         int32_t valid;
-        const char* src = source(u, c, &valid);
+        int64_t before;
+        const char* src = source(u, c, &valid, &before);
         dma16(valid > 0 ? src : zero, base + buf + c * 4096 + wave * 1024);
     };
     // One half-step: the matrix instructions of fragment set kk; between them the reads of
@@ -764,8 +782,9 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 #pragma unroll
             for (int c = 0; c < 2 * NB; ++c) {
                 int32_t valid;
-                const char* src = source(u, c, &valid);
-                stage[c] = load_chunk<ELEM>(src, valid);
+                int64_t before;
+                const char* src = source(u, c, &valid, &before);
+                stage[c] = load_chunk<ELEM>(src, valid, before);
             }
         };
         for (;;) {
@@ -808,8 +827,9 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
 // Tokens to int8 codes: step = max |x| / 127 (float32), code = rint(x / step), the division IEEE.
 // A row with a NaN or an infinity gets step NaN and zero codes, so that it spoils its own
-// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out): a workgroup per row, which is
-// read once and kept in registers up to 8,192 elements, in chunks of 16 bytes at any alignment.
+// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out): one wave per row, no barrier; the row
+// is read once and kept in registers up to 8 chunks of 16 bytes a lane.  WHOLE: the rows are
+// whole aligned chunks; else chunks at any alignment, the last one short.
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
     if constexpr (sizeof(T) == 4)
@@ -817,55 +837,81 @@ __device__ __forceinline__ float to_f32(T v) {
     else
         return __uint_as_float((uint32_t)v << 16);
 }
-constexpr int kQuantKeep = 4;  // chunks a thread keeps
+// Largest |x| of a chunk, +inf where one is NaN or infinite.
 template <typename T>
+__device__ __forceinline__ float chunk_max(v4i v) {
+    constexpr int NV = 16 / sizeof(T);
+    T e[NV];
+    __builtin_memcpy(e, &v, 16);
+    float m = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+        const float f = fabsf(to_f32(e[r]));
+        bad |= !(f < INFINITY);
+        m = fmaxf(m, f);
+    }
+    return bad ? INFINITY : m;
+}
+// rint(x / s) for the elements of a chunk.  With inv = 1 / s, t = x inv is off from the quotient by less than
+// 2e-5 (|x / s| <= 127, three roundings of 2^-24), so where t lies further than 5e-5 from the middle between
+// whole numbers rint(t) is rint of the IEEE quotient; else, or where 1 / s overflows, the chunk is
+// divided (one in 600 chunks of 8).
+template <typename T>
+__device__ __forceinline__ void chunk_codes(v4i v, float s, float inv, int8_t* q) {
+    constexpr int NV = 16 / sizeof(T);
+    T e[NV];
+    __builtin_memcpy(e, &v, 16);
+    float n[NV], off = 0.0f;
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+        const float t = to_f32(e[r]) * inv;
+        n[r] = rintf(t);
+        off = fmaxf(off, fabsf(t - n[r]));
+    }
+    if (!(off < 0.49995f) || !(s > 1e-37f)) {
+#pragma unroll
+        for (int r = 0; r < NV; ++r) n[r] = s > 0.0f ? rintf(to_f32(e[r]) / s) : 0.0f;
+    }
+#pragma unroll
+    for (int r = 0; r < NV; ++r) q[r] = (int8_t)(int)fminf(fmaxf(n[r], -127.0f), 127.0f);
+}
+__device__ __forceinline__ float step_of(float m) { return m < INFINITY ? m / 127.0f : NAN; }
+
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(256) void i8_quantize_kernel(const T* x, int64_t n, int32_t d, int64_t xs, int8_t* codes,
                                                           float* scale) {
     constexpr int NV = 16 / sizeof(T);
-    __shared__ float red[4];
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x & 63;
     const int32_t chunks = (d + NV - 1) / NV;
-    for (int64_t row = blockIdx.x; row < n; row += gridDim.x) {
+    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < n; row += (int64_t)gridDim.x * 4) {
         const T* xr = x + row * xs;
         auto fetch = [&](int32_t c) -> v4i {
-            return load_chunk<sizeof(T)>(reinterpret_cast<const char*>(xr + (int64_t)c * NV),
-                                         ((int64_t)d - (int64_t)c * NV) * (int64_t)sizeof(T));
+            const T* p = xr + (int64_t)c * NV;
+            if constexpr (WHOLE)
+                return *reinterpret_cast<const v4i*>(p);
+            else
+                return load_chunk<sizeof(T)>(reinterpret_cast<const char*>(p), (int64_t)(d - c * NV) * (int)sizeof(T), (int64_t)c * 16);
         };
-        v4i keep[kQuantKeep];
+        constexpr int KEEP = WHOLE ? 8 : 1;
+        v4i keep[KEEP];
         float m = 0.0f;
-        bool bad = false;
-        auto look = [&](v4i v) {
-            T e[NV];
-            __builtin_memcpy(e, &v, 16);
 #pragma unroll
-            for (int r = 0; r < NV; ++r) {
-                const float f = fabsf(to_f32(e[r]));
-                bad |= !(f < INFINITY);
-                m = fmaxf(m, f);
-            }
-        };
+        for (int k = 0; k < KEEP; ++k)
+            if (lane + k * 64 < chunks) keep[k] = fetch(lane + k * 64);
 #pragma unroll
-        for (int k = 0; k < kQuantKeep; ++k)
-            if (tid + k * 256 < chunks) keep[k] = fetch(tid + k * 256);
-#pragma unroll
-        for (int k = 0; k < kQuantKeep; ++k)
-            if (tid + k * 256 < chunks) look(keep[k]);
-        for (int32_t c = tid + kQuantKeep * 256; c < chunks; c += 256) look(fetch(c));
+        for (int k = 0; k < KEEP; ++k)
+            if (lane + k * 64 < chunks) m = fmaxf(m, chunk_max<T>(keep[k]));
+        for (int32_t c = lane + KEEP * 64; c < chunks; c += 64) m = fmaxf(m, chunk_max<T>(fetch(c)));
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        if ((tid & 63) == 0) red[tid >> 6] = m;
-        const int any = __syncthreads_or(bad);  // also publishes red
-        const float s = any ? NAN : fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / 127.0f;
-        if (tid == 0) scale[row] = s;
+        const float s = step_of(m), inv = 1.0f / s;
+        if (lane == 0) scale[row] = s;
         auto write = [&](int32_t c, v4i v) {
-            T e[NV];
             int8_t q[NV];
-            __builtin_memcpy(e, &v, 16);
-#pragma unroll
-            for (int r = 0; r < NV; ++r)
-                q[r] = s > 0.0f ? (int8_t)(int)fminf(fmaxf(rintf(to_f32(e[r]) / s), -127.0f), 127.0f) : (int8_t)0;
+            chunk_codes<T>(v, s, inv, q);
             int8_t* o = codes + row * d + (int64_t)c * NV;
-            if ((int64_t)(c + 1) * NV <= d) {
+            if (WHOLE || (c + 1) * NV <= d) {
                 __builtin_memcpy(o, q, NV);
             } else {
 #pragma unroll
@@ -874,10 +920,208 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const T* x, int64_t n,
             }
         };
 #pragma unroll
-        for (int k = 0; k < kQuantKeep; ++k)
-            if (tid + k * 256 < chunks) write(tid + k * 256, keep[k]);
-        for (int32_t c = tid + kQuantKeep * 256; c < chunks; c += 256) write(c, fetch(c));
+        for (int k = 0; k < KEEP; ++k)
+            if (lane + k * 64 < chunks) write(lane + k * 64, keep[k]);
+        for (int32_t c = lane + KEEP * 64; c < chunks; c += 64) write(c, fetch(c));
+    }
+}
+
+// Few rows: the product is a single pass over the weights.  A workgroup has 16 columns of one matrix and 16 FR
+// rows at a time; its eight waves share out the sum, load their pieces of both operands from
+// memory into the matrix instruction's layout (lane 16 g + i: 16 bytes of row i), 4 x 64 bytes at once,
+// and add up through LDS in a fixed order.  XB = 2 or 4: Q holds tokens of that many bytes an
+// element, which every workgroup quantises for itself (as i8_quantize_kernel does, bit for bit).
+// HBM-bound in the weights where they are many (ROWS_US).
+constexpr int kRowWaves = 8;
+template <int MODE, int FR, bool WHOLE, int XB>
+__global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
+    constexpr int ELEM = MODE == kI8 ? 1 : 2, U = 4;
+    static_assert(XB == 0 || (MODE == kI8 && FR == 1 && WHOLE), "");
+    typedef typename Acc<MODE>::type acc_t;
+    __shared__ acc_t part[kRowWaves][FR][64];
+    __shared__ float most[kRowWaves][16];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, li = lane & 15;
+    const int32_t kb = (int32_t)a.red * ELEM, steps = (kb + 63) >> 6;
+    const int32_t s0 = steps * wave / kRowWaves, s1 = steps * (wave + 1) / kRowWaves;
+    const int32_t j = blockIdx.x * 16 + g * 4;  // this lane's four output columns
+    const int32_t leaf = MODE == kI8 ? 0 : blockIdx.y;
+    auto put = [&](int32_t row, v4f v) {
+        if (a.out_f32) {
+            float* o = static_cast<float*>(a.out) + row * a.J + j;
+            if (j + 4 <= a.J)
+                __builtin_memcpy(o, &v, 16);
+            else if (j < a.J)
+                store_left<4>(reinterpret_cast<char*>(o), __builtin_bit_cast(v4i, v), (int32_t)a.J - j);
+        } else {
+            uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.J + j;
+            const uint32_t w[2] = {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+            if (j + 4 <= a.J)
+                __builtin_memcpy(o, w, 8);
+            else if (j < a.J)
+                store_left<2>(reinterpret_cast<char*>(o), v4i{(int)w[0], (int)w[1], 0, 0}, (int32_t)a.J - j);
+        }
+    };
+    int32_t p0, p1;
+    if constexpr (MODE == kI8) {
+        p0 = blockIdx.y * 16 * FR;
+        p1 = p0 + 16 * FR < a.T ? p0 + 16 * FR : (int32_t)a.T;
+    } else if (leaf < a.L) {
+        p0 = leaf_start(a, leaf);
+        p1 = leaf_start(a, leaf + 1);
+    } else {  // rows of no leaf
+        if (blockIdx.z > 0) return;
+        const int32_t head = leaf_start(a, 0), tail = leaf_start(a, a.L);
+        for (int32_t p = tid >> 2; p < head + (int32_t)a.T - tail; p += kRowWaves * 16) {
+            const int32_t row = slot_of(a, p < head ? p : tail + p - head), c = blockIdx.x * 16 + (tid & 3) * 4;
+            if (row < 0 || c >= a.J) continue;
+            const int32_t left = (int32_t)a.J - c, ob = a.out_f32 ? 4 : 2;
+            char* o = static_cast<char*>(a.out) + (row * a.J + c) * ob;
+            for (int32_t e = 0; e < (left < 4 ? left : 4) * ob; e += 2) *reinterpret_cast<uint16_t*>(o + e) = 0;
+        }
+        return;
+    }
+    const int32_t col = blockIdx.x * 16 + li < a.J ? blockIdx.x * 16 + li : (int32_t)a.J - 1;
+    const char* const prow = a.p + leaf * a.pg + col * a.ps;
+    auto fetch = [&](const char* row, int32_t o) -> v4i {
+        v4i v = {0, 0, 0, 0};
+        if constexpr (WHOLE) {
+            if (o < kb) v = *reinterpret_cast<const v4i*>(row + o);
+        } else if (o < kb) {  // the last chunk is read as the row's last 16 bytes
+            const int cut = o + 16 > kb ? o + 16 - kb : 0;
+            __builtin_memcpy(&v, row + o - cut, 16);
+            v = shift_down(v, cut);
+        }
+        return v;
+    };
+    // the output's scales, asked for before the operands: at the end they would cost another trip
+    float sw[4] = {}, bias[4] = {};
+    if constexpr (MODE == kI8) {
+        if (wave < FR) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int32_t je = j + e < a.J ? j + e : (int32_t)a.J - 1;
+                sw[e] = a.sw[je];
+                bias[e] = a.bias ? a.bias[je] : 0.0f;
+            }
+        }
+    }
+    for (int32_t p = p0 + blockIdx.z * 16 * FR; p < p1; p += gridDim.z * 16 * FR) {
+        int32_t out_row[FR];
+        const char* qrow[FR];
+        float sx = 0.0f;  // of the rows that this wave stores (fragment `wave`)
+#pragma unroll
+        for (int f = 0; f < FR; ++f) {
+            int32_t r = p + f * 16 + li;
+            const bool in = r < p1;
+            if (!in) r = p;  // rows past the last repeat the first; they are not written
+            if constexpr (MODE == kI8) {
+                out_row[f] = in ? r : -1;
+                if (XB == 0 && wave == f) sx = a.sx[r];
+            } else {
+                r = slot_of(a, r);
+                out_row[f] = in ? r : -1;
+                r = r < 0 ? 0 : (int32_t)query_of(a, (uint32_t)r);
+            }
+            qrow[f] = a.q + (int64_t)r * a.qs;
+        }
+        v4i pv[U], qv[U][FR], xv[XB > 0 ? U : 1][XB > 0 ? XB : 1];
+        auto load = [&](int32_t s) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s + u < s1) {
+                    const int32_t o = (s + u) * 64 + g * 16;
+                    if constexpr (XB == 0) {
+#pragma unroll
+                        for (int f = 0; f < FR; ++f) qv[u][f] = fetch(qrow[f], o);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < XB; ++c)
+                            xv[u][c] = o < kb ? *reinterpret_cast<const v4i*>(qrow[0] + (o * XB + c * 16)) : v4i{0, 0, 0, 0};
+                    }
+                    pv[u] = fetch(prow, o);
+                }
+        };
+        load(s0);
+        if constexpr (XB > 0) {
+            float m = 0.0f;
+            auto look = [&](v4i v) {
+                if constexpr (XB == 2)
+                    m = fmaxf(m, chunk_max<uint16_t>(v));
+                else
+                    m = fmaxf(m, chunk_max<float>(v));
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s0 + u < s1) {
+#pragma unroll
+                    for (int c = 0; c < XB; ++c) look(xv[u][c]);
+                }
+            for (int32_t s = s0 + U; s < s1; ++s) {
+                const int32_t o = s * 64 + g * 16;
+                if (o < kb) {
+#pragma unroll
+                    for (int c = 0; c < XB; ++c) look(*reinterpret_cast<const v4i*>(qrow[0] + (o * XB + c * 16)));
+                }
+            }
+            m = fmaxf(m, __shfl_xor(m, 16, 64));
+            m = fmaxf(m, __shfl_xor(m, 32, 64));
+            most[wave][li] = m;
+            __syncthreads();
+            m = most[0][li];
+#pragma unroll
+            for (int w = 1; w < kRowWaves; ++w) m = fmaxf(m, most[w][li]);
+            sx = step_of(m);
+        }
+        acc_t acc[FR];
+#pragma unroll
+        for (int f = 0; f < FR; ++f) acc[f] = acc_t{0, 0, 0, 0};
+        for (int32_t s = s0; s < s1; s += U) {
+            if (s > s0) load(s);
+            if constexpr (XB > 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (s + u < s1) {
+                        int8_t q[16];
+#pragma unroll
+                        for (int c = 0; c < XB; ++c) {
+                            if constexpr (XB == 2)
+                                chunk_codes<uint16_t>(xv[u][c], sx, 1.0f / sx, q + c * 8);
+                            else
+                                chunk_codes<float>(xv[u][c], sx, 1.0f / sx, q + c * 4);
+                        }
+                        __builtin_memcpy(&qv[u][0], q, 16);
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s + u < s1) {
+#pragma unroll
+                    for (int f = 0; f < FR; ++f) acc[f] = mma<MODE>(pv[u], qv[u][f], acc[f]);
+                }
+        }
+#pragma unroll
+        for (int f = 0; f < FR; ++f) part[wave][f][lane] = acc[f];
         __syncthreads();
+#pragma unroll
+        for (int f = 0; f < FR; ++f)
+            if (wave == f && out_row[f] >= 0) {
+                acc_t t = part[0][f][lane];
+#pragma unroll
+                for (int w = 1; w < kRowWaves; ++w) t += part[w][f][lane];
+                v4f v;
+                if constexpr (MODE == kI8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = (float)t[e] * sx * sw[e];
+                        if (a.bias) v[e] += bias[e];
+                    }
+                } else {
+                    v = t;
+                }
+                put(out_row[f], v);
+            }
+        if (p + (int32_t)gridDim.z * 16 * FR < p1) __syncthreads();
     }
 }
 
@@ -955,6 +1199,30 @@ hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Row fragments of prod_rows_kernel, or 0 for the tiled kernel.
+template <int MODE>
+int row_fragments(const ProdArgs& a) {
+    const int64_t rows = MODE == kI8 ? a.T : (a.T + a.L - 1) / a.L;  // of one matrix, on average
+    if (a.L >= 65535 || a.red * (MODE == kI8 ? 1 : 2) < 16) return 0;  // the grid's second dimension; a row's last 16 bytes
+    if (MODE == kI8) return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
+    return rows <= 6 ? 1 : rows <= 14 ? 2 : rows <= 48 ? 4 : 0;  // leaves differ: room for twice the average
+}
+
+template <int MODE, int FR, int XB = 0>
+hipError_t launch_rows(const ProdArgs& a, bool whole, hipStream_t stream) {
+    // a leaf's rows beyond 16 FR go to a second workgroup
+    const dim3 grid((uint32_t)((a.J + 15) / 16), (uint32_t)(MODE == kI8 ? (a.T + 16 * FR - 1) / (16 * FR) : a.L + 1),
+                    MODE == kI8 || a.T / a.L < 8 ? 1 : 2);
+    if constexpr (XB == 0) {
+        if (!whole) {
+            hipLaunchKernelGGL((prod_rows_kernel<MODE, FR, false, 0>), grid, dim3(kRowWaves * 64), 0, stream, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((prod_rows_kernel<MODE, FR, true, XB>), grid, dim3(kRowWaves * 64), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <int MODE>
 hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     const int e = MODE == kI8 ? 1 : 2;
@@ -972,6 +1240,13 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     a.fan_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + fan - 1) / fan);
     const int64_t pitch = a.J * (a.out_f32 ? 4 : 2);
     a.bypass = MODE != kFwd && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
+    if constexpr (MODE == kI8 || MODE == kFwd) {
+        switch (row_fragments<MODE>(a)) {
+            case 1: return launch_rows<MODE, 1>(a, whole, stream);
+            case 2: return launch_rows<MODE, 2>(a, whole, stream);
+            case 4: return launch_rows<MODE, 4>(a, whole, stream);
+        }
+    }
     if (!whole) return launch_tiles<MODE, 2, 2, false>(a, stream);
     if constexpr (MODE == kDw) {
         return launch_tiles<MODE, 2, 2, true>(a, stream);
@@ -988,18 +1263,22 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
 
 hipError_t launch_i8_quantize(const void* x, int32_t dtype, int64_t n, int32_t d, int64_t xs, int8_t* codes,
                               float* scale, hipStream_t stream) {
-    const uint32_t wgs = (uint32_t)(n < 65536 ? n : 65536);
+    const int64_t e = dtype == AH_F32 ? 4 : 2;
+    const dim3 grid((uint32_t)(n < (1 << 22) ? (n + 3) / 4 : 1 << 20));
+    const bool whole = chunked(x, xs * e, d * e);
+    auto go = [&](auto kernel, auto* rows) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, rows, n, d, xs, codes, scale);
+    };
     if (dtype == AH_F32)
-        hipLaunchKernelGGL(i8_quantize_kernel<float>, dim3(wgs), dim3(256), 0, stream, static_cast<const float*>(x), n,
-                           d, xs, codes, scale);
+        go(whole ? i8_quantize_kernel<float, true> : i8_quantize_kernel<float, false>, static_cast<const float*>(x));
     else
-        hipLaunchKernelGGL(i8_quantize_kernel<uint16_t>, dim3(wgs), dim3(256), 0, stream,
-                           static_cast<const uint16_t*>(x), n, d, xs, codes, scale);
+        go(whole ? i8_quantize_kernel<uint16_t, true> : i8_quantize_kernel<uint16_t, false>,
+           static_cast<const uint16_t*>(x));
     return hipGetLastError();
 }
 
-hipError_t launch_i8_matmul(const int8_t* x8, const float* xs, int64_t m, const int8_t* w8, const float* ws, int64_t n,
-                            int32_t k, const float* bias, void* out, int32_t out_dtype, hipStream_t stream) {
+static ProdArgs i8_args(const int8_t* x8, const float* xs, int64_t m, const int8_t* w8, const float* ws, int64_t n,
+                        int32_t k, const float* bias, void* out, int32_t out_dtype) {
     ProdArgs a{};
     a.q = reinterpret_cast<const char*>(x8);
     a.p = reinterpret_cast<const char*>(w8);
@@ -1012,7 +1291,12 @@ hipError_t launch_i8_matmul(const int8_t* x8, const float* xs, int64_t m, const 
     a.sx = xs;
     a.sw = ws;
     a.bias = bias;
-    return launch_prod<kI8>(a, 1, stream);
+    return a;
+}
+
+hipError_t launch_i8_matmul(const int8_t* x8, const float* xs, int64_t m, const int8_t* w8, const float* ws, int64_t n,
+                            int32_t k, const float* bias, void* out, int32_t out_dtype, hipStream_t stream) {
+    return launch_prod<kI8>(i8_args(x8, xs, m, w8, ws, n, k, bias, out, out_dtype), 1, stream);
 }
 
 // Workspace: the tokens' codes (rows of k bytes, the block rounded up to 16) and their steps.
@@ -1022,6 +1306,12 @@ size_t i8_linear_workspace_bytes(int64_t m, int32_t k) { return code_bytes(m, k)
 hipError_t launch_i8_linear(const void* x, int32_t dtype, int64_t m, int32_t k, int64_t xs, const int8_t* w8,
                             const float* ws, int64_t n, const float* bias, void* out, int32_t out_dtype, void* work,
                             hipStream_t stream) {
+    const int64_t bytes = dtype == AH_F32 ? 4 : 2;
+    if (m <= 16 && chunked(x, xs * bytes, k) && chunked(w8, k, 0)) {
+        ProdArgs a = i8_args(static_cast<const int8_t*>(x), nullptr, m, w8, ws, n, k, bias, out, out_dtype);
+        a.qs = xs * bytes;
+        return dtype == AH_F32 ? launch_rows<kI8, 1, 4>(a, true, stream) : launch_rows<kI8, 1, 2>(a, true, stream);
+    }
     int8_t* codes = static_cast<int8_t*>(work);
     float* scale = reinterpret_cast<float*>(codes + code_bytes(m, k));
     const hipError_t e = launch_i8_quantize(x, dtype, m, k, xs, codes, scale, stream);
