@@ -508,12 +508,12 @@ int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64
  *   logits   [n] rows of V elements of dtype, stride apart;  ids int32 [n][k];  scores float32 [n][k]
  *   row_weight float32 [n] (the gradient of the total with respect to each row's loss) or NULL = 1
  *   loss_out float32 [n];  grad_out of dtype, rows grad_stride apart, or NULL; may be logits itself
- *   workspace >= ah_distill_workspace_bytes(n, V) bytes, 16-byte aligned
+ *   workspace >= ah_distill_workspace_bytes(n, V, k) bytes, 16-byte aligned
  * Errors: AH_ERR_SHAPE (n < 0, V, k < 1, a stride < V, tau not positive and finite),
- * AH_ERR_UNSUPPORTED (dtype, k > AH_MAX_R, V >= 2^31, tau outside 1e-30 .. 1e30, workspace not
+ * AH_ERR_UNSUPPORTED (dtype, k > AH_MAX_R, n or V >= 2^31, tau outside 1e-30 .. 1e30, workspace not
  * aligned), AH_ERR_NULL, AH_ERR_WORKSPACE.
  */
-size_t ah_distill_workspace_bytes(int64_t n, int64_t V);
+size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k);
 int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
                     const float* scores, int32_t k, float tau, const float* row_weight, float* loss_out,
                     void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream);

@@ -137,7 +137,7 @@ def lib() -> C.CDLL:
         L.ah_grouped_matmul_dw.restype = C.c_int
         L.ah_grouped_matmul_dw.argtypes = [vp, i64, vp, i64, i32, i32, i32, vp, vp, i64, i32, vp, i32, vp]
         L.ah_distill_workspace_bytes.restype = sz
-        L.ah_distill_workspace_bytes.argtypes = [i64, i64]
+        L.ah_distill_workspace_bytes.argtypes = [i64, i64, i32]
         L.ah_distill_topk.restype = C.c_int
         L.ah_distill_topk.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp]
         L.ah_scan_topk_noalloc.restype = C.c_int
@@ -822,8 +822,8 @@ def ah_grouped_matmul_dw(dy, x, offsets, order=None, fan=1, out_dtype=torch.floa
     return dw_out
 
 
-def ah_distill_workspace_bytes(n: int, V: int) -> int:
-    return int(lib().ah_distill_workspace_bytes(n, V))
+def ah_distill_workspace_bytes(n: int, V: int, k: int) -> int:
+    return int(lib().ah_distill_workspace_bytes(n, V, k))
 
 
 def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=True, loss_out=None, grad_out=None,
@@ -847,7 +847,7 @@ def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=Tru
             raise ValueError("grad_out must have the shape of logits")
     elif want_grad:
         grad_out = _empty((n, V), logits.dtype, logits.device, stream)
-    workspace = _work(workspace, ah_distill_workspace_bytes(n, V), "workspace", logits.device, stream)
+    workspace = _work(workspace, ah_distill_workspace_bytes(n, V, ids.shape[1]), "workspace", logits.device, stream)
     _check(lib().ah_distill_topk(_at(logits), dt, n, V, zs, _at(ids), _at(scores), ids.shape[1], float(tau),
                                  _at(row_weight), _at(loss_out), _at(grad_out), gs, _at(workspace),
                                  _nbytes(workspace), _on(stream, logits)), "ah_distill_topk")

@@ -481,9 +481,9 @@ int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64
     return hip_status(ah::launch_grouped_dw(g, dw_out, out_dtype, static_cast<hipStream_t>(stream)));
 }
 
-size_t ah_distill_workspace_bytes(int64_t n, int64_t V) {
-    if (n < 0 || V < 1) return 0;
-    return ah::distill_workspace_bytes(n, V);
+size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k) {
+    if (n < 0 || V < 1 || k < 1) return 0;
+    return ah::distill_workspace_bytes(n, V, k);
 }
 
 int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
@@ -491,10 +491,11 @@ int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int
                     void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream) {
     if (n < 0 || V < 1 || stride < V || k < 1 || !(tau > 0.0f) || !(tau < 1e30f) || (grad_out && grad_stride < V))
         return AH_ERR_SHAPE;
-    if (!float_type(dtype) || k > AH_MAX_R || V >= ((int64_t)1 << 31) || tau < 1e-30f) return AH_ERR_UNSUPPORTED;
+    if (!float_type(dtype) || k > AH_MAX_R || V >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31) ||
+        tau < 1e-30f) return AH_ERR_UNSUPPORTED;
     if (n == 0) return AH_OK;
     if (!logits || !ids || !scores || !loss_out) return AH_ERR_NULL;
-    const size_t need = ah::distill_workspace_bytes(n, V);
+    const size_t need = ah::distill_workspace_bytes(n, V, k);
     if (need > 0 && (!workspace || workspace_bytes < need)) return AH_ERR_WORKSPACE;
     if (need > 0 && !a16(workspace)) return AH_ERR_UNSUPPORTED;
     return hip_status(ah::launch_distill(logits, dtype, n, V, stride, ids, scores, k, tau, row_weight, loss_out,

@@ -130,7 +130,7 @@ hipError_t launch_grouped_dx(const GroupedProblem& g, void* out, int32_t out_dty
 hipError_t launch_grouped_dw(const GroupedProblem& g, void* out, int32_t out_dtype, hipStream_t stream);
 
 // Distillation from a teacher's (ids, scores): loss and gradient.
-size_t distill_workspace_bytes(int64_t n, int64_t V);
+size_t distill_workspace_bytes(int64_t n, int64_t V, int32_t k);
 hipError_t launch_distill(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
                           const float* scores, int32_t k, float tau, const float* weight, float* loss, void* grad,
                           int64_t grad_stride, void* ws, hipStream_t stream);
