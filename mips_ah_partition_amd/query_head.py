@@ -1,0 +1,83 @@
+"""QueryHead: the learned side of an index, from a model's hidden states to its queries.
+
+A frozen linear layer in int8 (the last layer of an encoder) makes features; a
+router sends each feature vector to its best leaves (the centroid scoring that a
+partitioned search starts with); every leaf has its own projection, and a query is
+the sum of its leaves' projections weighted by the softmax of their scores.  The
+projections are trained against answers that an index gave, (ids, scores) as every
+search here returns them: the head's own scores of all items, the int8 score plane
+of the flat search, are pulled towards the teacher's by the distillation loss.
+
+All products, the routing, the loss and the gradients are the C-ABI calls
+ah_i8_linear, ah_partition_score, ah_group_rows, ah_grouped_matmul (_dx, _dw) and
+ah_distill_topk; torch keeps the memory and does the elementwise arithmetic.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import ahlib
+
+
+class QueryHead:
+    def __init__(self, trunk: torch.Tensor, router: torch.Tensor, dim: int, fan: int = 2, seed: int = 0):
+        """trunk: float32 [k, h], the frozen layer's weights (h: the hidden width); router: float32
+        [L, k], one centroid a leaf; dim: the index's dimension; fan: leaves a query goes through."""
+        self.trunk8, self.trunk_scale = ahlib.ah_i8_quantize_rows(trunk)
+        self.router = router.contiguous()
+        L, k = router.shape
+        if trunk.shape[0] != k or not 1 <= fan <= L:
+            raise ValueError("trunk and router differ in width, or fan is not in 1..leaves")
+        self.fan = int(fan)
+        g = torch.Generator(device=router.device)
+        g.manual_seed(seed)
+        self.weights = torch.randn(L, dim, k, generator=g, device=router.device) * k ** -0.5  # float32 master copy
+        self.w = self.weights.bfloat16()
+        self._kept = None
+
+    def queries(self, hidden: torch.Tensor, keep: bool = False) -> torch.Tensor:
+        """Queries float32 [m, dim] of hidden states (bfloat16 or float32 [m, h]); keep: hold what
+        `step` needs of this forward pass."""
+        x = ahlib.ah_i8_linear(hidden, self.trunk8, self.trunk_scale, out_dtype=torch.bfloat16)
+        leaves, scores = ahlib.ah_partition_score(x.float(), self.router, self.fan)
+        offsets, order = ahlib.ah_group_rows(leaves, self.router.shape[0])
+        y = ahlib.ah_grouped_matmul(x, self.w, offsets, order=order, fan=self.fan, out_dtype=torch.float32)
+        gate = torch.softmax(scores, dim=1)
+        if keep:
+            self._kept = (x, offsets, order, gate)
+        return (y.view(*gate.shape, -1) * gate[:, :, None]).sum(1)
+
+    def step(self, hidden, items, ids, scores, tau: float = 1.0, lr: float = 0.1, want_dx: bool = False):
+        """One step of training on a batch: items is an `Items`, ids / scores the teacher's answers
+        (int32 / float32 [m, k]).  Returns (losses float32 [m], gradient of the features or None)."""
+        m = hidden.shape[0]
+        q = self.queries(hidden, keep=True)
+        x, offsets, order, gate = self._kept
+        self._kept = None
+        # bfloat16 scores: the gradient that leaves the loss is the next product's operand
+        z = ahlib.ah_i8_linear(q, items.codes, items.step, out_dtype=torch.bfloat16)
+        weight = torch.full((m,), 1.0 / m, device=q.device)
+        loss, dz = ahlib.ah_distill_topk(z, ids, scores, tau=tau, row_weight=weight, grad_out=z)
+        one = torch.tensor([0, m], dtype=torch.int64, device=q.device)
+        dq = ahlib.ah_grouped_matmul(dz, items.columns[None], one, out_dtype=torch.float32)
+        dy = (gate[:, :, None] * dq[:, None, :]).to(torch.bfloat16).reshape(m * self.fan, -1)
+        dw = ahlib.ah_grouped_matmul_dw(dy, x, offsets, order=order, fan=self.fan)
+        dx = None
+        if want_dx:
+            dx = ahlib.ah_grouped_matmul_dx(dy, self.w, offsets, order=order, fan=self.fan)
+        self.weights.add_(dw, alpha=-lr)
+        self.w.copy_(self.weights)
+        return loss, dx
+
+
+class Items:
+    """What a head is trained to score: rows float32 [n, d] as int8 codes and steps, and their
+    values by column (bfloat16 [d, n]) for the gradient."""
+
+    def __init__(self, rows: torch.Tensor):
+        self.codes, self.step = ahlib.ah_i8_quantize_rows(rows)
+        n, d = rows.shape
+        self.columns = torch.empty(d, n, dtype=torch.bfloat16, device=rows.device)
+        for a in range(0, n, 1 << 16):
+            part = slice(a, a + (1 << 16))
+            self.columns[:, part] = (self.codes[part].float() * self.step[part, None]).t().to(torch.bfloat16)
