@@ -15,10 +15,13 @@
 // every operand's step is cut into blocks of 8 KB: 64 rows x 128 bytes ("row" operands)
 // or 64 memory rows x 64 columns ("by column").  Global memory goes straight to LDS (16
 // bytes a lane); that write is linear in the lane, so the swizzle that keeps the reads
-// free of bank conflicts is applied to the source address: a row operand's 16-byte
-// chunk c of row r lies at c ^ key(r), a by-column operand's 32-byte granule c of memory
-// row r at c ^ (r >> 1 & 1 | (r >> 3 & 1) << 1): the eight rows that are read at
-// once then lie in eight different places.  The matrix instruction takes P as its A operand, so
+// free of bank conflicts is applied to the source address.  A row operand's 16-byte
+// chunk c of row r lies at c ^ key(r).  A 16-byte read serves lanes 0-3, 12-15, 20-23 and 24-27 at
+// once (then 4-11, 16-19, 28-31, and the upper half alike), so key has to tell apart rows 0-3 from
+// 12-15 and 4-7 from 8-11 of a fragment read in order, and the same of rows 8 a + b (PERM):
+// r & 3 with the parity of bits 2 and 4 above it does (0 conflicts counted; r & 7, without
+// PERM, too).  A by-column operand's 32-byte granule c of memory row r lies at c ^ (r >> 1 & 1 | (r >> 3
+// & 1) << 1).  The matrix instruction takes P as its A operand, so
 // that a lane ends with four consecutive output columns of one row.
 #include "ah_device.hpp"
 #include "ah_kernels.hpp"
@@ -470,7 +473,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     // This thread's 16-byte chunks, two of each block: rows 32 s + rr (of a row operand) or memory rows
     // 32 s + rr (by column), at byte rc or cc of the row.
-    auto key = [](int r) { return (r & 3) | (((r >> 2) ^ (r >> 3)) & 1) << 2; };
+    auto key = [](int r) { return (r & 3) | (((r >> 2) ^ (r >> 4)) & 1) << 2; };
     auto ckey = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 1) << 1; };
     const int rr = tid >> 3, rc = ((tid & 7) ^ key(rr)) * 16;
     const int cc = ((((tid & 7) >> 1) ^ ckey(rr)) << 1 | (tid & 1)) * 16;
@@ -621,14 +624,14 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             return by_col(pcol[x] + buf, kk * 4096);
         else if constexpr (PERM)  // four rows on, the key's high bit changes: the other start
             return by_row(pstart[kk ^ (x & 1)] + buf, (x >> 1) * 4096 + (x & 1) * 512);
-        else
-            return by_row(pstart[kk] + buf, x * 2048);
+        else  // 16 rows on likewise
+            return by_row(pstart[kk ^ (x & 1)] + buf, x * 2048);
     };
     auto read_q = [&](int x, int kk, uint32_t buf) -> v4i {
         if constexpr (QCOL)
             return by_col(qcol[x] + buf, kk * 4096);
         else
-            return by_row(qstart[kk] + buf, x * 2048);
+            return by_row(qstart[kk ^ (x & 1)] + buf, x * 2048);
     };
 
     typedef typename Acc<MODE>::type acc_t;
