@@ -10,7 +10,8 @@
 //   few (slice, leaf) counts         two: the slices' histograms, and the places, where every
 //                                    workgroup adds up the histograms for itself
 //   else                             three: a scan over the slices, one wave a leaf, between them
-// Bound by launches and by the latency of a run's loads, which are all started at once (GROUP_US).
+// Bound by launches and by the latency of a run's loads, which are all started at once: 32,768
+// slots of 64 leaves 5 + 6 us.
 #include "ah_device.hpp"
 #include "ah_kernels.hpp"
 #include "../../include/ah.h"

@@ -379,6 +379,13 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // 4 x 4 (256 x 256, all accumulation registers, one wave a SIMD) loads 64 KB for 512 matrix
 // instructions, 3 x 4 an eighth more and 2 x 2 (two workgroups a CU) twice that for each of
 // them; tile_shape below chooses.
+// Measured: int8 8192 x 4096 x 16384 480 us (2.29 POP/s) of a 497-520 us call; 1000 x 1536 x 100003 to float32
+// 257 us (400 MB of outputs at an odd pitch); bfloat16 32,768 rows of 64 leaves, 1536 -> 4096, 540 us (763
+// TFLOP/s); 16,384 rows of 16 leaves, 1536 x 1536: dx 114 us, dw 175.  Bound by the power limit and by the
+// step's LDS reads: a loop of these matrix instructions alone holds 1.97 GHz on random values (1935 bfloat16
+// TFLOP/s; zeros 2.40 GHz), with the LDS reads of a step 1661; the int8 kernel runs at 1.9 GHz, the bfloat16
+// one at 1.4 to 1.6.  Without the loads, the barrier or the wait for them (8192 x 6144 x 4096, bfloat16) 360, 422
+// and 442 us instead of 446, on zeros 337.
 template <int MODE, int NQ, int NP, int OB, bool DMA>
 __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(ProdArgs a) {
     constexpr int ELEM = MODE == kI8 ? 1 : 2, FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
@@ -485,34 +492,58 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     uint32_t qoff[MODE == kI8 ? 2 * NQ : 1];
     int32_t slot[SLOTS];                  // slots of a tile's rows; dw: of the next step's memory rows
 
+    // What the order holds is kept as it was read until it is used, a step later: a check beside the
+    // load would wait for it, load by load.
+    auto known = [&](int32_t s) { return s >= 0 && s < a.T; };
     // dw: the memory rows of step u of tile n come from the order (load_slots), and are turned into
-    // addresses when the step's loads start (set_rows).
+    // addresses when the step's loads start (set_rows, w being the tile).
     auto load_slots = [&](const Tile& n, int u, int32_t(&to)[SLOTS]) {
+        int32_t in[2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int32_t r = u * STEP + s * 32 + rr, in = r < n.red ? n.p0 + r : n.p0 < a.T ? n.p0 : 0;
-            const int32_t v = a.order ? a.order[in] : in;
-            to[s] = r < n.red && v < a.T ? v : -1;
+            const int32_t r = u * STEP + s * 32 + rr;
+            to[s] = in[s] = r < n.red ? n.p0 + r : n.p0 < a.T ? n.p0 : 0;
+        }
+        if (a.order) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) to[s] = a.order[in[s]];
         }
     };
-    auto set_rows = [&](const int32_t(&from)[SLOTS]) {
+    auto set_rows = [&](int u, const int32_t(&from)[SLOTS]) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            qrow[s] = from[s] < 0 ? nullptr : a.q + (int64_t)from[s] * a.qs + (int64_t)w.i0 * 2 + cc;
+            const bool is = u * STEP + s * 32 + rr < w.red && known(from[s]);
+            qrow[s] = is ? a.q + (int64_t)from[s] * a.qs + (int64_t)w.i0 * 2 + cc : nullptr;
             prow[s] = a.p + (int64_t)query_of(a, (uint32_t)from[s]) * a.ps + (int64_t)w.j0 * 2 + cc;
         }
     };
-    // A tile's rows: first what has to be read (slots, output rows: lane's and 64 + lane's of this wave's
-    // part, -1: not written), later the addresses.
+    // A tile's rows: first what has to be read (slots of its rows, and of lane's and 64 + lane's row of
+    // this wave's part, where the results go), later the addresses.
     auto take_rows = [&](const Tile& n, int32_t(&rows)[2]) {
-        const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7, rr = tid >> 3;
         if constexpr (RAGGED) {
+            const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7, rr = tid >> 3;
+            const int32_t some = n.p0 < a.T ? n.p0 : 0;  // rows past the tile repeat its first
+            int32_t in[2 * NQ + 2];
 #pragma unroll
-            for (int s = 0; s < 2 * NQ; ++s) {
-                const int32_t r = n.p0 + s * 32 + rr;
-                slot[s] = slot_of(a, r < n.p1 ? r : n.p0 < a.T ? n.p0 : 0);  // rows past the tile repeat its first
+            for (int s = 0; s < 2 * NQ + 2; ++s) {
+                const int32_t r = n.p0 + (s < 2 * NQ ? s * 32 + rr : wq * 32 * NQ + (s - 2 * NQ) * 64 + lane);
+                in[s] = r < n.p1 ? r : some;
+            }
+#pragma unroll
+            for (int s = 0; s < 2 * NQ; ++s) slot[s] = in[s];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) rows[u] = in[2 * NQ + u];
+            if (a.order) {
+#pragma unroll
+                for (int s = 0; s < 2 * NQ; ++s) slot[s] = a.order[in[s]];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) rows[u] = a.order[in[2 * NQ + u]];
             }
         }
+    };
+    // Output rows of tile n, of which rows holds what take_rows read; -1: not written.
+    auto out_rows = [&](const Tile& n, int32_t(&rows)[2]) {
+        const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int32_t i = wq * 32 * NQ + u * 64 + lane;
@@ -521,7 +552,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             else if constexpr (MODE == kI8)
                 rows[u] = n.p0 + i < n.p1 ? n.p0 + i : -1;
             else
-                rows[u] = n.p0 + i < n.p1 ? slot_of(a, n.p0 + i) : -1;
+                rows[u] = n.p0 + i < n.p1 && known(rows[u]) ? rows[u] : -1;
         }
     };
     auto set_addresses = [&]() {
@@ -536,7 +567,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         } else if constexpr (!QCOL) {
 #pragma unroll
             for (int s = 0; s < 2 * NQ; ++s) {
-                int32_t r = slot[s] < 0 ? 0 : slot[s];
+                int32_t r = known(slot[s]) ? slot[s] : 0;
                 if constexpr (MODE == kFwd) r = (int32_t)query_of(a, (uint32_t)r);
                 qrow[s] = a.q + (int64_t)r * a.qs + rc;
             }
@@ -693,7 +724,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     __syncthreads();
     if constexpr (DMA) {
         Tile ws = uniform(sh.next[0]);  // the order's cursor: tile, its step, its rows
-        int32_t us = 0, rows_s[2];
+        int32_t us = 0, rows_s[2] = {};
         int64_t ts = t;
         int k = 1;
         take_rows(ws, rows_s);
@@ -723,9 +754,9 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         for (; ul < 2; ++ul) {
             if constexpr (MODE == kDw) {
                 if (ul == 0)
-                    set_rows(slot);
+                    set_rows(0, slot);
                 else
-                    set_rows(slot1);
+                    set_rows(1, slot1);
             }
 #pragma unroll
             for (int c = 0; c < 2 * NB; ++c) load(ul, c, ul * BUF);
@@ -759,11 +790,12 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                 for (int u = 0; u < 2; ++u) rows_l[u] = rows_s[u];
                 set_addresses();
             }
-            if constexpr (MODE == kDw) set_rows(slot);
+            if constexpr (MODE == kDw) set_rows(ul, slot);
             advance_order();
             half_step(1, BUF - cur, ul++);
             if (++uc < wc.nt) continue;
             if constexpr (NQ * NP > 4) settle();
+            out_rows(wc, rows_c);
             store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows_c, wc.leaf, wc.j0);
             t += hop;
             if (t >= tend) break;
@@ -775,12 +807,12 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         }
         land<0>();  // no load is left in flight towards LDS
     } else {
-        int32_t rows[2];
+        int32_t rows[2] = {};
         v4i stage[2 * NB];
         auto fetch = [&](int u) {
             if constexpr (MODE == kDw) {
                 load_slots(w, u, slot);
-                set_rows(slot);
+                set_rows(u, slot);
             }
 #pragma unroll
             for (int c = 0; c < 2 * NB; ++c) {
@@ -818,6 +850,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                         acc[m / FP][m % FP] = mma<MODE>(pf[kk][m % FP], qf[kk][m / FP], acc[m / FP][m % FP]);
                 }
             }
+            out_rows(w, rows);
             store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows, w.leaf, w.j0);
             t += hop;
             if (t >= tend) break;
@@ -830,7 +863,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
 // Tokens to int8 codes: step = max |x| / 127 (float32), code = rint(x / step), the division IEEE.
 // A row with a NaN or an infinity gets step NaN and zero codes, so that it spoils its own
-// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out): one wave per row, no barrier; the row
+// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out; bfloat16 8192 x 4096: 23 us, 4.4 TB/s): one wave
+// per row, no barrier; the row
 // is read once and kept in registers up to 8 chunks of 16 bytes a lane.  WHOLE: the rows are
 // whole aligned chunks; else chunks at any alignment, the last one short.
 template <typename T>
@@ -934,7 +968,9 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const T* x, int64_t n,
 // memory into the matrix instruction's layout (lane 16 g + i: 16 bytes of row i), 4 x 64 bytes at once,
 // and add up through LDS in a fixed order.  XB = 2 or 4: Q holds tokens of that many bytes an
 // element, which every workgroup quantises for itself (as i8_quantize_kernel does, bit for bit).
-// HBM-bound in the weights where they are many (ROWS_US).
+// HBM-bound in the weights where they are many: 64 slots of 64 leaves, 1536 x 1536, 189 MB of weights
+// in 34 us for grouping and product (5.6 TB/s); one token, 1536 -> 4096, 9.5 us a call, a launch's
+// latency (15.6 with tiles and quantising in a launch of its own).
 constexpr int kRowWaves = 8;
 template <int MODE, int FR, bool WHOLE, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
@@ -1128,7 +1164,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
     }
 }
 
-// Sum of each row's `fan` float32 partial gradients, rounded once.  HBM-bound; four columns a thread
+// Sum of each row's `fan` float32 partial gradients, rounded once.  HBM-bound (8192 rows x 2 x 1536 to float32:
+// 22 us, 6.9 TB/s, part of it from the last-level cache); four columns a thread
 // (cols % 4 == 0: the partial rows are 16-byte aligned; else one).
 template <int N>
 __global__ __launch_bounds__(256) void fan_sum_kernel(const float* part, int64_t rows, int32_t fan, int64_t cols,
