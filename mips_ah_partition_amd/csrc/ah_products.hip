@@ -380,7 +380,7 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // instructions, 3 x 4 an eighth more and 2 x 2 (two workgroups a CU) twice that for each of
 // them; tile_shape below chooses.
 // Measured: int8 8192 x 4096 x 16384 480 us (2.29 POP/s) of a 497-520 us call; 1000 x 1536 x 100003 to float32
-// 257 us (400 MB of outputs at an odd pitch); bfloat16 32,768 rows of 64 leaves, 1536 -> 4096, 540 us (763
+// 257 us (400 MB of outputs at an odd pitch); bfloat16 32,768 rows of 64 leaves, 1536 -> 4096, 520 us (793
 // TFLOP/s); 16,384 rows of 16 leaves, 1536 x 1536: dx 114 us, dw 175.  Bound by the power limit and by the
 // step's LDS reads: a loop of these matrix instructions alone holds 1.97 GHz on random values (1935 bfloat16
 // TFLOP/s; zeros 2.40 GHz), with the LDS reads of a step 1661; the int8 kernel runs at 1.9 GHz, the bfloat16
