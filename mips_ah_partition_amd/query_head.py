@@ -38,22 +38,32 @@ class QueryHead:
     def queries(self, hidden: torch.Tensor, keep: bool = False) -> torch.Tensor:
         """Queries float32 [m, dim] of hidden states (bfloat16 or float32 [m, h]); keep: hold what
         `step` needs of this forward pass."""
+        q, x, _, offsets, order, gate, _ = self._forward(hidden)
+        if keep:
+            self._kept = (x, offsets, order, gate)
+        return q
+
+    def _forward(self, hidden):
+        """Queries, features bfloat16 [m, k], leaves [m, fan], the slots' order, gates float32 [m, fan] and
+        the slots' projections float32 [m, fan, dim]."""
         x = ahlib.ah_i8_linear(hidden, self.trunk8, self.trunk_scale, out_dtype=torch.bfloat16)
         leaves, scores = ahlib.ah_partition_score(x.float(), self.router, self.fan)
         offsets, order = ahlib.ah_group_rows(leaves, self.router.shape[0])
         y = ahlib.ah_grouped_matmul(x, self.w, offsets, order=order, fan=self.fan, out_dtype=torch.float32)
         gate = torch.softmax(scores, dim=1)
-        if keep:
-            self._kept = (x, offsets, order, gate)
-        return (y.view(*gate.shape, -1) * gate[:, :, None]).sum(1)
+        y = y.view(*gate.shape, self.w.shape[1])
+        return (y * gate[:, :, None]).sum(1), x, leaves, offsets, order, gate, y
 
     def step(self, hidden, items, ids, scores, tau: float = 1.0, lr: float = 0.1, want_dx: bool = False):
         """One step of training on a batch: items is an `Items`, ids / scores the teacher's answers
-        (int32 / float32 [m, k]).  Returns (losses float32 [m], gradient of the features or None)."""
+        (int32 / float32 [m, k]).  Returns (losses float32 [m], gradient of the features or None).
+
+        The gradient (bfloat16 [m, k], of the mean loss) is that of the features x in
+        q = sum_f softmax(router x)_f W_f x: through the projections and through the gates, with the choice
+        of leaves held.  The rounding of queries to int8 codes in the score plane counts as
+        the identity."""
         m = hidden.shape[0]
-        q = self.queries(hidden, keep=True)
-        x, offsets, order, gate = self._kept
-        self._kept = None
+        q, x, leaves, offsets, order, gate, y = self._forward(hidden)
         # bfloat16 scores: the gradient that leaves the loss is the next product's operand
         z = ahlib.ah_i8_linear(q, items.codes, items.step, out_dtype=torch.bfloat16)
         weight = torch.full((m,), 1.0 / m, device=q.device)
@@ -64,7 +74,13 @@ class QueryHead:
         dw = ahlib.ah_grouped_matmul_dw(dy, x, offsets, order=order, fan=self.fan)
         dx = None
         if want_dx:
-            dx = ahlib.ah_grouped_matmul_dx(dy, self.w, offsets, order=order, fan=self.fan)
+            dx = ahlib.ah_grouped_matmul_dx(dy, self.w, offsets, order=order, fan=self.fan, out_dtype=torch.float32)
+            # the gates: d gate_f / d score_g = gate_f ([f = g] - gate_g), score_f = router[leaf_f] . x
+            along = (y * dq[:, None, :]).sum(2)
+            dscore = gate * (along - (gate * along).sum(1, keepdim=True))
+            dscore = torch.where(leaves >= 0, dscore, torch.zeros_like(dscore))  # no leaf, no score
+            dx += (dscore[:, :, None] * self.router[leaves.clamp(min=0).long()]).sum(1)
+            dx = dx.to(torch.bfloat16)
         self.weights.add_(dw, alpha=-lr)
         self.w.copy_(self.weights)
         return loss, dx
