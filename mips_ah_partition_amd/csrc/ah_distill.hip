@@ -421,21 +421,40 @@ void cut(int64_t n, int64_t V, int64_t elem, int32_t* slices, int64_t* slice) {
     *slices = (int32_t)((V + *slice - 1) / *slice);
 }
 
+// The call's next rows, after the first a.n.
+template <typename T>
+void next_rows(DistillArgs& a) {
+    a.z = static_cast<const T*>(a.z) + a.n * a.zs;
+    a.ids += a.n * a.k;
+    a.t += a.n * a.k;
+    if (a.weight) a.weight += a.n;
+    a.loss += a.n;
+    if (a.grad) a.grad = static_cast<T*>(a.grad) + a.n * a.gs;
+}
+
 template <typename T>
 hipError_t launch(DistillArgs a, void* ws, hipStream_t stream) {
-    const int64_t bytes = a.V * (int64_t)sizeof(T);
+    const int64_t bytes = a.V * (int64_t)sizeof(T), all = a.n;
     const uint32_t lds = 128 + 12 * (((uint32_t)a.k + 3) & ~3u);
     if (!split_rows(a.n, bytes)) {
-        const dim3 grid((uint32_t)a.n);
-        if (bytes <= (16 << 10) + 15)
-            hipLaunchKernelGGL((distill_row_kernel<T, 256, 4>), grid, dim3(256), lds, stream, a);
-        else if (bytes <= (64 << 10) + 15)
-            hipLaunchKernelGGL((distill_row_kernel<T, 512, 8>), grid, dim3(512), lds, stream, a);
-        else
-            hipLaunchKernelGGL((distill_row_kernel<T, 512, 16>), grid, dim3(512), lds, stream, a);
-        return hipGetLastError();
+        const int nt = bytes <= (16 << 10) + 15 ? 256 : 512;
+        const int64_t most = kMaxGridItems / nt;  // rows of one launch
+        for (int64_t r = 0; r < all; r += most) {
+            a.n = all - r < most ? all - r : most;
+            const dim3 grid((uint32_t)a.n);
+            if (nt == 256)
+                hipLaunchKernelGGL((distill_row_kernel<T, 256, 4>), grid, dim3(256), lds, stream, a);
+            else if (bytes <= (64 << 10) + 15)
+                hipLaunchKernelGGL((distill_row_kernel<T, 512, 8>), grid, dim3(512), lds, stream, a);
+            else
+                hipLaunchKernelGGL((distill_row_kernel<T, 512, 16>), grid, dim3(512), lds, stream, a);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            next_rows<T>(a);
+        }
+        return hipSuccess;
     }
-    const int64_t all = a.n, group = kCacheBytes / bytes < 1 ? 1 : kCacheBytes / bytes;
+    const int64_t group = kCacheBytes / bytes < 1 ? 1 : kCacheBytes / bytes;
     for (int64_t r = 0; r < all; r += group) {
         a.n = all - r < group ? all - r : group;
         cut(a.n, a.V, sizeof(T), &a.slices, &a.slice);
@@ -446,12 +465,7 @@ hipError_t launch(DistillArgs a, void* ws, hipStream_t stream) {
         hipLaunchKernelGGL(distill_grad_kernel<T>, grid, dim3(kST), lds, stream, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        a.z = static_cast<const T*>(a.z) + a.n * a.zs;
-        a.ids += a.n * a.k;
-        a.t += a.n * a.k;
-        if (a.weight) a.weight += a.n;
-        a.loss += a.n;
-        if (a.grad) a.grad = static_cast<T*>(a.grad) + a.n * a.gs;
+        next_rows<T>(a);
     }
     return hipSuccess;
 }

@@ -98,6 +98,9 @@ hipError_t launch_reorder(const float* q, int64_t nq, int32_t d, const void* bas
                           int64_t n, const int32_t* cand, int32_t R, int32_t k, int32_t* ids,
                           float* scores, hipStream_t stream);
 
+// Work-items that one dimension of a launch may have: HIP takes fewer than 2^32.
+constexpr int64_t kMaxGridItems = ((int64_t)1 << 32) - 1;
+
 // Int8 products with a scale for each token and channel.
 hipError_t launch_i8_quantize(const void* x, int32_t dtype, int64_t n, int32_t d, int64_t xs, int8_t* codes,
                               float* scale, hipStream_t stream);

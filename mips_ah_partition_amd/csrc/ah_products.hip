@@ -1230,7 +1230,7 @@ hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
         const int64_t leaf = (a.I + TQ - 1) / TQ * np;
         if (leaf >= 8) wgs = (leaf + 7) / 8 * 8 * a.L;
     }
-    if ((MODE != kDw || wgs >= ((int64_t)1 << 31)) && wgs > resident) wgs = resident;
+    if ((MODE != kDw || wgs * kNT > kMaxGridItems) && wgs > resident) wgs = resident;
     const dim3 grid((uint32_t)wgs);
     if (a.out_f32)
         hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 4, DMA>), grid, dim3(kNT), 0, stream, a);
@@ -1239,10 +1239,15 @@ hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Whether prod_rows_kernel's grid, a workgroup for every 16 columns, can be launched; the tiled kernel takes
+// any number of columns.
+inline bool rows_launchable(int64_t J) { return (J + 15) / 16 * (kRowWaves * 64) <= kMaxGridItems; }
+
 // Row fragments of prod_rows_kernel, or 0 for the tiled kernel.
 template <int MODE>
 int row_fragments(const ProdArgs& a) {
     const int64_t rows = MODE == kI8 ? a.T : (a.T + a.L - 1) / a.L;  // of one matrix, on average
+    if (!rows_launchable(a.J)) return 0;
     if (a.L >= 65535 || a.red * (MODE == kI8 ? 1 : 2) < 16) return 0;  // the grid's second dimension; a row's last 16 bytes
     if (MODE == kI8) return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 0;
     return rows <= 6 ? 1 : rows <= 14 ? 2 : rows <= 48 ? 4 : 0;  // leaves differ: room for twice the average
@@ -1347,7 +1352,7 @@ hipError_t launch_i8_linear(const void* x, int32_t dtype, int64_t m, int32_t k, 
                             const float* ws, int64_t n, const float* bias, void* out, int32_t out_dtype, void* work,
                             hipStream_t stream) {
     const int64_t bytes = dtype == AH_F32 ? 4 : 2;
-    if (m <= 16 && chunked(x, xs * bytes, k) && chunked(w8, k, 0)) {
+    if (m <= 16 && rows_launchable(n) && chunked(x, xs * bytes, k) && chunked(w8, k, 0)) {
         ProdArgs a = i8_args(static_cast<const int8_t*>(x), nullptr, m, w8, ws, n, k, bias, out, out_dtype);
         a.qs = xs * bytes;
         return dtype == AH_F32 ? launch_rows<kI8, 1, 4>(a, true, stream) : launch_rows<kI8, 1, 2>(a, true, stream);

@@ -1,0 +1,93 @@
+"""The learned query side's calls at the ends of the sizes that they accept, and in the kernel variants that only
+larger products reach, against plain forms in 64 bits.
+
+Tolerances as for the other tests of these calls.  int8: bit for bit.  Grouped products: a float32 sum of t
+exact products is off by at most t 2^-23 sum |a||b|, its rounding by 2^-8 (bfloat16) or 2^-23
+relative.  Distillation: a few (1 + |z / tau|) 2^-23 for the exponentials, 2^-8 for a bfloat16 gradient.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+E = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mips_ah_partition_amd import ahlib
+    ahlib.lib()
+    yield torch, ahlib
+    torch.cuda.empty_cache()
+
+
+# --------------------------------------------------------------------------- more workgroups than a launch can have
+@pytest.mark.parametrize("m", [1, 20])
+def test_int8_rows_against_more_columns_than_a_row_launch_has(gpu, m):
+    """16 columns a workgroup of 512 threads would be 2^32 work-items from 2^27 columns on."""
+    torch, ah = gpu
+    k, n = 16, (1 << 27) + 1000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    w8 = torch.randint(-127, 128, (n, k), device="cuda", dtype=torch.int8, generator=g)
+    ws = torch.rand(n, device="cuda", generator=g)
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    c, s = ah.ah_i8_quantize_rows(x)
+    y = ah.ah_i8_linear(x, w8, ws)
+    z = ah.ah_i8_matmul(c, s, w8, ws, out_dtype=torch.bfloat16)
+    for j in range(0, n, 1 << 24):
+        part = slice(j, j + (1 << 24))
+        dot = torch.mm(c.float(), w8[part].float().t())  # whole numbers below 2^24
+        ref = ((dot * s[:, None]) * ws[None, part]).bfloat16()
+        assert torch.equal(y[:, part], ref) and torch.equal(z[:, part], ref)
+
+
+def test_distillation_of_more_rows_than_a_launch_has(gpu):
+    """A workgroup of 256 threads a row would be 2^32 work-items from 2^24 rows on."""
+    torch, ah = gpu
+    n, V, k = (1 << 24) + 9, 16, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    z = torch.randn(n, V, device="cuda", generator=g).bfloat16()
+    ids = torch.randint(-1, V, (n, k), device="cuda", dtype=torch.int32, generator=g)
+    sc = torch.randn(n, k, device="cuda", generator=g)
+    w = torch.rand(n, device="cuda", generator=g)
+    loss, grad = ah.ah_distill_topk(z, ids, sc, row_weight=w)
+    for r in range(0, n, 1 << 21):
+        part = slice(r, r + (1 << 21))
+        zd, ok = z[part].double(), ids[part] >= 0
+        lq = torch.log_softmax(zd, 1)
+        some = ok.any(1)
+        t = torch.where(ok, sc[part].double(), torch.full_like(sc[part].double(), -float("inf")))
+        lp = torch.log_softmax(torch.where(some[:, None], t, torch.zeros_like(t)), 1)
+        p = torch.where(ok, lp.exp(), torch.zeros_like(lp))
+        at = ids[part].clamp(min=0).long()
+        want = torch.where(ok, p * (lp - lq.gather(1, at)), torch.zeros_like(p)).sum(1)
+        dz = (lq.exp() * some[:, None]).scatter_add(1, at, -p) * w[part].double()[:, None]
+        size = 1 + zd.abs().amax(1) + sc[part].double().abs().amax(1)
+        assert ((loss[part].double() - want).abs() <= 40 * E * size * (size + 3)).all()
+        assert ((grad[part].double() - dz).abs() <= 40 * E * size[:, None] + 2.0 ** -8 * dz.abs()).all()
+
+
+def test_weight_gradients_of_more_tiles_than_a_launch_has(gpu):
+    """65,536 leaves of 256 tiles each: a workgroup of 256 threads a tile would be 2^32 work-items."""
+    torch, ah = gpu
+    L, n, k, rows = 1 << 16, 1 << 15, 1, 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    leaf = torch.randint(0, L, (rows,), device="cuda", generator=g)
+    leaf[:3], leaf[3:40] = torch.tensor([0, L - 1, L - 1], device="cuda"), 777
+    order = torch.sort(leaf, stable=True).indices.to(torch.int32)
+    off = torch.searchsorted(torch.sort(leaf).values, torch.arange(L + 1, device="cuda"))
+    x, dy = (torch.randn(rows, c, device="cuda", generator=g).bfloat16() for c in (k, n))
+    dw = ah.ah_grouped_matmul_dw(dy, x, off, order=order, out_dtype=torch.bfloat16)
+    left = sum(int(torch.count_nonzero(part)) for part in dw.split(4096))
+    for l in leaf.unique().tolist():
+        at = (leaf == l).nonzero().flatten()
+        terms = dy[at].double() * x[at].double()
+        want, got = terms.sum(0), dw[l, :, 0].double()
+        assert ((got - want).abs() <= (rows + 2) * E * terms.abs().sum(0) + 2.0 ** -8 * want.abs()).all()
+        left -= int(torch.count_nonzero(dw[l]))
+    assert left == 0  # leaves without a row
