@@ -510,7 +510,7 @@ int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64
  *   loss_out float32 [n];  grad_out of dtype, rows grad_stride apart, or NULL; may be logits itself
  *   workspace >= ah_distill_workspace_bytes(n, V, k) bytes, 16-byte aligned
  * Errors: AH_ERR_SHAPE (n < 0, V, k < 1, a stride < V, tau not positive and finite),
- * AH_ERR_UNSUPPORTED (dtype, k > AH_MAX_R, n or V >= 2^31, tau outside 1e-30 .. 1e30, workspace not
+ * AH_ERR_UNSUPPORTED (dtype, k > AH_MAX_R, n or V >= 2^31, tau < 1e-30 or >= 1e30, workspace not
  * aligned), AH_ERR_NULL, AH_ERR_WORKSPACE.
  */
 size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k);

@@ -489,10 +489,10 @@ size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k) {
 int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
                     const float* scores, int32_t k, float tau, const float* row_weight, float* loss_out,
                     void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream) {
-    if (n < 0 || V < 1 || stride < V || k < 1 || !(tau > 0.0f) || !(tau < 1e30f) || (grad_out && grad_stride < V))
+    if (n < 0 || V < 1 || stride < V || k < 1 || !(tau > 0.0f) || !(tau < INFINITY) || (grad_out && grad_stride < V))
         return AH_ERR_SHAPE;
     if (!float_type(dtype) || k > AH_MAX_R || V >= ((int64_t)1 << 31) || n >= ((int64_t)1 << 31) ||
-        tau < 1e-30f) return AH_ERR_UNSUPPORTED;
+        tau < 1e-30f || tau >= 1e30f) return AH_ERR_UNSUPPORTED;
     if (n == 0) return AH_OK;
     if (!logits || !ids || !scores || !loss_out) return AH_ERR_NULL;
     const size_t need = ah::distill_workspace_bytes(n, V, k);
