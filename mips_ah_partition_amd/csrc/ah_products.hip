@@ -405,28 +405,33 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     // Row tiles.  Ragged: a prefix sum of the leaves' row tiles from the leaf starts on the device,
     // one entry or a run of them per thread, kept in registers: this thread's entries have
-    // the row tiles [first, last).
+    // the row tiles [first, last).  Starts in order make at most T / TQ tiles and one more for each entry; starts
+    // out of order are held to that, by thread and in all, so that no count passes 32 bits and every
+    // tile that is walked belongs to a thread.
     const int32_t E = a.L + 2, run = (E + kNT - 1) / kNT;
-    int32_t first = 0, last = 0;
+    uint32_t first = 0, last = 0;
     int64_t nq = MODE == kDw ? (a.I + TQ - 1) / TQ : (a.T + TQ - 1) / TQ;
     if constexpr (RAGGED) {
+        const int32_t whole = (int32_t)(a.T / TQ);
         int32_t sum = 0;
         for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
             int32_t b, n;
             entry_rows(a, e, &b, &n);
             sum += (n + TQ - 1) / TQ;
+            sum = sum < whole + run ? sum : whole + run;
         }
-        last = wave_inclusive_sum(sum);
-        if (lane == 63) sh.wave_sum[wave] = last;
+        last = (uint32_t)wave_inclusive_sum(sum);
+        if (lane == 63) sh.wave_sum[wave] = (int32_t)last;
         __syncthreads();
         nq = 0;
 #pragma unroll
         for (int w = 0; w < kNT / 64; ++w) {
             const int32_t s = sh.wave_sum[w];
-            if (w < wave) last += s;
+            if (w < wave) last += (uint32_t)s;
             nq += s;
         }
-        first = last - sum;
+        first = last - (uint32_t)sum;
+        nq = nq < whole + E ? nq : whole + E;
         nq = __builtin_amdgcn_readfirstlane((int32_t)nq);
     }
     // dw: a leaf's tiles cost what the leaf has rows, so every XCD takes an eighth of each leaf's tiles (of
@@ -443,8 +448,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             if (tid == 0) sh.next[k] = Tile{-1, 0, 0, 0, 0, 0, 0x7fffffff};
         } else if constexpr (RAGGED) {
             walk(t, nq, np, &tq, &tp);
-            if (tq >= first && tq < last) {
-                int32_t at = first;
+            if ((uint32_t)tq >= first && (uint32_t)tq < last) {
+                int32_t at = (int32_t)first;
                 for (int32_t e = tid * run; e < E && e < (tid + 1) * run; ++e) {
                     int32_t b, n;
                     entry_rows(a, e, &b, &n);

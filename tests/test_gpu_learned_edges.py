@@ -91,3 +91,24 @@ def test_weight_gradients_of_more_tiles_than_a_launch_has(gpu):
         assert ((got - want).abs() <= (rows + 2) * E * terms.abs().sum(0) + 2.0 ** -8 * want.abs()).all()
         left -= int(torch.count_nonzero(dw[l]))
     assert left == 0  # leaves without a row
+
+
+# --------------------------------------------------------------------------- leaf starts that are not in order
+def test_grouped_starts_out_of_order_walk_no_more_tiles_than_rows_have(gpu):
+    """Starts 0, T, 0, T, ...: 32,768 leaves of all T rows each, 2^31 row tiles by their count.  No output is
+    promised, but nothing outside the arrays is touched and the call ends."""
+    torch, ah = gpu
+    T, L, w = 1 << 23, 1 << 16, 8
+    off = torch.zeros(L + 1, device="cuda", dtype=torch.int64)
+    off[1::2] = T
+    x = torch.ones(T, w, device="cuda", dtype=torch.bfloat16)
+    mats = torch.ones(L, w, w, device="cuda", dtype=torch.bfloat16)
+    guard = torch.full((T + 2, w), 3.0, device="cuda", dtype=torch.float32)
+    ah.ah_grouped_matmul(x, mats, off, out=guard[1:T + 1])
+    ah.ah_grouped_matmul_dx(x, mats, off, dx_out=guard[1:T + 1])
+    torch.cuda.synchronize()
+    assert (guard[0] == 3).all() and (guard[T + 1] == 3).all()
+    # and in order again, every leaf 128 rows
+    off = torch.arange(L + 1, device="cuda", dtype=torch.int64) * (T // L)
+    y = ah.ah_grouped_matmul(x, mats, off, out_dtype=torch.float32)
+    assert (y == w).all()
