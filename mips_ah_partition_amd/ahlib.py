@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libah.so")
 AH_OK, AH_ERR_NULL, AH_ERR_SHAPE, AH_ERR_UNSUPPORTED, AH_ERR_WORKSPACE, AH_ERR_HIP = 0, -1, -2, -3, -4, -5
 AH_F32, AH_BF16 = 0, 1
 AH_CODES_TILED = -1
+AH_MAX_WIDTH = 1 << 20  # n and k of the grouped products
 
 # every symbol include/ah.h declares
 EXPORTS = (

@@ -69,7 +69,10 @@ class QueryHead:
         weight = torch.full((m,), 1.0 / m, device=q.device)
         loss, dz = ahlib.ah_distill_topk(z, ids, scores, tau=tau, row_weight=weight, grad_out=z)
         one = torch.tensor([0, m], dtype=torch.int64, device=q.device)
-        dq = ahlib.ah_grouped_matmul(dz, items.columns[None], one, out_dtype=torch.float32)
+        dq = None
+        for a, part in items.parts():  # a product sums at most 2^20 items; more are added up in order
+            d = ahlib.ah_grouped_matmul(dz[:, a:a + part.shape[1]], part[None], one, out_dtype=torch.float32)
+            dq = d if dq is None else dq.add_(d)
         dy = (gate[:, :, None] * dq[:, None, :]).to(torch.bfloat16).reshape(m * self.fan, -1)
         dw = ahlib.ah_grouped_matmul_dw(dy, x, offsets, order=order, fan=self.fan)
         dx = None
@@ -88,12 +91,28 @@ class QueryHead:
 
 class Items:
     """What a head is trained to score: rows float32 [n, d] as int8 codes and steps, and their
-    values by column (bfloat16 [d, n]) for the gradient."""
+    values by column (bfloat16, [d, at most 2^20] a part) for the gradient.  A step on m queries keeps
+    their scores of all items, m n bfloat16 values."""
+
+    MOST = ahlib.AH_MAX_WIDTH  # items of a part
 
     def __init__(self, rows: torch.Tensor):
         self.codes, self.step = ahlib.ah_i8_quantize_rows(rows)
         n, d = rows.shape
-        self.columns = torch.empty(d, n, dtype=torch.bfloat16, device=rows.device)
-        for a in range(0, n, 1 << 16):
-            part = slice(a, a + (1 << 16))
-            self.columns[:, part] = (self.codes[part].float() * self.step[part, None]).t().to(torch.bfloat16)
+        self._parts = []
+        for a in range(0, max(n, 1), self.MOST):
+            b = min(n, a + self.MOST)
+            columns = torch.empty(d, b - a, dtype=torch.bfloat16, device=rows.device)
+            for c in range(a, b, 1 << 16):
+                part = slice(c, min(b, c + (1 << 16)))
+                columns[:, c - a:part.stop - a] = (self.codes[part].float() * self.step[part, None]).t().to(torch.bfloat16)
+            self._parts.append(columns)
+
+    def parts(self):
+        """(first item, values by column) of each part."""
+        return [(i * self.MOST, columns) for i, columns in enumerate(self._parts)]
+
+    @property
+    def columns(self) -> torch.Tensor:
+        """The values of all items by column, bfloat16 [d, n] (put together where there are several parts)."""
+        return self._parts[0] if len(self._parts) == 1 else torch.cat(self._parts, dim=1)

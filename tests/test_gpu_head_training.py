@@ -77,3 +77,59 @@ def test_gradient_of_the_features(gpu, m, fan):
     assert ((dx.to(D) - want).abs() <= 4 * 2.0 ** -8 * size).all()
     # the roundings are independent of each other: in norm they stay near one bfloat16 step
     assert float((dx.to(D) - want).norm()) <= 0.05 * float(want.norm())
+
+
+def _weight_gradient(torch, ah, head, items, hidden, ids, sc, tau):
+    """The weights' gradient in 64 bits from the head's own queries on, and the sizes of its terms."""
+    D, m = torch.float64, hidden.shape[0]
+    q = head.queries(hidden, keep=True)
+    x, _, _, gate = head._kept
+    leaves = ah.ah_partition_score(x.float(), head.router, head.fan)[0].long()
+    z = ah.ah_i8_linear(q, items.codes, items.step, out_dtype=torch.bfloat16).to(D)
+    dz = torch.softmax(z / tau, 1).scatter_add(1, ids.long(), -torch.softmax(sc.to(D) / tau, 1)) * tau / m
+    it = items.columns.to(D)
+    dq, dqa = torch.mm(dz, it.t()), torch.mm(dz.abs(), it.abs().t())
+    want, size = (torch.zeros(head.w.shape, dtype=D, device="cuda") for _ in range(2))
+    for f in range(head.fan):
+        for l in range(head.w.shape[0]):
+            at = (leaves[:, f] == l).nonzero().flatten()
+            gf = gate[at, f, None].to(D)
+            want[l] += torch.mm((gf * dq[at]).t(), x[at].to(D))
+            size[l] += torch.mm((gf * dqa[at]).t(), x[at].to(D).abs())
+    return want, size
+
+
+def test_items_beyond_one_product(gpu):
+    """More items than a product sums at once: 2^20."""
+    torch, ah, qh = gpu
+    m, d, n = 5, 16, (1 << 20) + 1000
+    head, items, hidden, rnd = _setup(torch, qh, m, h=32, k=24, d=d, L=3, n=n)
+    assert items.columns.shape == (d, n)
+    ids, sc = _teacher(torch, items, rnd, m, d)
+    ids[:, 0] = torch.arange(n - m, n, device="cuda", dtype=torch.int32)  # of the last part
+    want, size = _weight_gradient(torch, ah, head, items, hidden, ids, sc, 2.0)
+    before = head.weights.clone()
+    loss, _ = head.step(hidden, items, ids, sc, tau=2.0, lr=1.0)
+    got = (before - head.weights).double()
+    assert torch.isfinite(loss).all()
+    assert ((got - want).abs() <= 4 * 2.0 ** -8 * size + 2.0 ** -22 * before.abs()).all()
+    assert float((got - want).norm()) <= 0.05 * float(want.norm())
+
+
+@pytest.mark.parametrize("most", [64, 256, 696])
+def test_items_in_parts_give_the_gradient_of_all(gpu, most, monkeypatch):
+    torch, ah, qh = gpu
+    m, d, n = 40, 48, 700
+    head, items, hidden, rnd = _setup(torch, qh, m, d=d, n=n)
+    ids, sc = _teacher(torch, items, rnd, m, d)
+    monkeypatch.setattr(qh.Items, "MOST", most)
+    again, cut, _, _ = _setup(torch, qh, m, d=d, n=n)
+    assert len(cut.parts()) == -(-n // most) and torch.equal(cut.columns, items.columns)
+    want, size = _weight_gradient(torch, ah, head, items, hidden, ids, sc, 2.0)
+    before = head.weights.clone()
+    l0, dx0 = head.step(hidden, items, ids, sc, tau=2.0, lr=1.0, want_dx=True)
+    l1, dx1 = again.step(hidden, cut, ids, sc, tau=2.0, lr=1.0, want_dx=True)
+    assert torch.equal(l0, l1)
+    for h in (head, again):
+        assert (((before - h.weights).double() - want).abs() <= 4 * 2.0 ** -8 * size + 2.0 ** -22 * before.abs()).all()
+    assert float((dx0 - dx1).float().norm()) <= 0.02 * float(dx0.float().norm())
