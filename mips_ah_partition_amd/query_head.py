@@ -68,7 +68,8 @@ class QueryHead:
         z = ahlib.ah_i8_linear(q, items.codes, items.step, out_dtype=torch.bfloat16)
         weight = torch.full((m,), 1.0 / m, device=q.device)
         loss, dz = ahlib.ah_distill_topk(z, ids, scores, tau=tau, row_weight=weight, grad_out=z)
-        one = torch.tensor([0, m], dtype=torch.int64, device=q.device)
+        one = torch.full((2,), m, dtype=torch.int64, device=q.device)  # one leaf, [0, m); made on the device,
+        one[:1].zero_()                                                # so that a graph can hold the step
         dq = None
         for a, part in items.parts():  # a product sums at most 2^20 items; more are added up in order
             d = ahlib.ah_grouped_matmul(dz[:, a:a + part.shape[1]], part[None], one, out_dtype=torch.float32)

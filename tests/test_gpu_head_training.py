@@ -133,3 +133,26 @@ def test_items_in_parts_give_the_gradient_of_all(gpu, most, monkeypatch):
     for h in (head, again):
         assert (((before - h.weights).double() - want).abs() <= 4 * 2.0 ** -8 * size + 2.0 ** -22 * before.abs()).all()
     assert float((dx0 - dx1).float().norm()) <= 0.02 * float(dx0.float().norm())
+
+
+def test_step_in_a_graph(gpu):
+    torch, ah, qh = gpu
+    m, d = 70, 48
+    head, items, hidden, rnd = _setup(torch, qh, m)
+    other = _setup(torch, qh, m)[0]
+    ids, sc = _teacher(torch, items, rnd, m, d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        head.step(hidden, items, ids, sc, lr=0.0, want_dx=True)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, dx = head.step(hidden, items, ids, sc, tau=2.0, lr=0.5, want_dx=True)
+    for i in range(4):
+        hidden.copy_(rnd(*hidden.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wdx = other.step(hidden, items, ids, sc, tau=2.0, lr=0.5, want_dx=True)
+        assert torch.equal(loss, want) and torch.equal(dx, wdx)
+        assert torch.equal(head.weights, other.weights) and torch.equal(head.w, other.w)
