@@ -66,7 +66,7 @@ class QueryHead:
         q, x, leaves, offsets, order, gate, y = self._forward(hidden)
         # bfloat16 scores: the gradient that leaves the loss is the next product's operand
         z = ahlib.ah_i8_linear(q, items.codes, items.step, out_dtype=torch.bfloat16)
-        weight = torch.full((m,), 1.0 / m, device=q.device)
+        weight = torch.full((m,), 1.0 / max(m, 1), device=q.device)
         loss, dz = ahlib.ah_distill_topk(z, ids, scores, tau=tau, row_weight=weight, grad_out=z)
         one = torch.full((2,), m, dtype=torch.int64, device=q.device)  # one leaf, [0, m); made on the device,
         one[:1].zero_()                                                # so that a graph can hold the step
@@ -74,7 +74,7 @@ class QueryHead:
         for a, part in items.parts():  # a product sums at most 2^20 items; more are added up in order
             d = ahlib.ah_grouped_matmul(dz[:, a:a + part.shape[1]], part[None], one, out_dtype=torch.float32)
             dq = d if dq is None else dq.add_(d)
-        dy = (gate[:, :, None] * dq[:, None, :]).to(torch.bfloat16).reshape(m * self.fan, -1)
+        dy = (gate[:, :, None] * dq[:, None, :]).to(torch.bfloat16).reshape(m * self.fan, q.shape[1])
         dw = ahlib.ah_grouped_matmul_dw(dy, x, offsets, order=order, fan=self.fan)
         dx = None
         if want_dx:

@@ -156,3 +156,12 @@ def test_step_in_a_graph(gpu):
         want, wdx = other.step(hidden, items, ids, sc, tau=2.0, lr=0.5, want_dx=True)
         assert torch.equal(loss, want) and torch.equal(dx, wdx)
         assert torch.equal(head.weights, other.weights) and torch.equal(head.w, other.w)
+
+
+def test_step_without_a_row(gpu):
+    torch, ah, qh = gpu
+    head, items, hidden, _ = _setup(torch, qh, 4)
+    before = head.weights.clone()
+    loss, dx = head.step(hidden[:0], items, torch.empty((0, 5), dtype=torch.int32, device="cuda"),
+                         torch.empty((0, 5), device="cuda"), want_dx=True)
+    assert loss.shape == (0,) and dx.shape == (0, 64) and torch.equal(head.weights, before)
