@@ -23,8 +23,6 @@
 namespace ah {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
 template <typename T>
 __device__ __forceinline__ float score_f32(T v) {
     if constexpr (sizeof(T) == 4)
@@ -47,6 +45,7 @@ struct DistillArgs {
     const float* t;
     int32_t k;
     float tau, inv_tau;
+    float c;  // log2(e) / tau, rounded once: exponents scale by it, so its error grows with them
     const float* weight;
     float* loss;
     void* grad;
@@ -276,7 +275,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
         }
     }
     wg_max2<NT>(m, tm, sh.red);
-    const float c = a.inv_tau * kLog2e, M = top(m);
+    const float c = a.c, M = top(m);
     float s = exp2_fast((last - M) * c), ts = entry_sum<NT>(a, sh, tm);
 #pragma unroll
     for (int u = 0; u < KEEP; ++u) {
@@ -315,7 +314,7 @@ __global__ __launch_bounds__(kST) void distill_part_kernel(DistillArgs a) {
     const int64_t row = blockIdx.x / (uint32_t)a.slices, sl = blockIdx.x % (uint32_t)a.slices;
     const int64_t v0 = sl * a.slice, v1 = v0 + a.slice < a.V ? v0 + a.slice : a.V;
     const T* z = static_cast<const T*>(a.z) + row * a.zs;
-    const float c = a.inv_tau * kLog2e;
+    const float c = a.c;
     const int64_t full = (v1 - v0) / C::N;
     float m = -INFINITY, s = 0.0f;
     constexpr int U = 4;
@@ -371,7 +370,7 @@ __global__ __launch_bounds__(kST) void distill_grad_kernel(DistillArgs a) {
         if (gr) clear_grads<T, kST>(gr, v0, v1);
         return;
     }
-    const float c = a.inv_tau * kLog2e;
+    const float c = a.c;
     const float* part = a.part + row * a.slices * 2;
     float m = -INFINITY, s = 0.0f;
     for (int32_t i = tid; i < a.slices; i += kST) m = fmaxf(m, part[2 * i]);
@@ -492,8 +491,9 @@ size_t distill_workspace_bytes(int64_t n, int64_t V, int32_t k) {
 hipError_t launch_distill(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
                           const float* scores, int32_t k, float tau, const float* weight, float* loss, void* grad,
                           int64_t grad_stride, void* ws, hipStream_t stream) {
-    const DistillArgs a{logits, n, V, stride, ids, scores, k, tau, 1.0f / tau, weight, loss, grad, grad_stride, nullptr,
-                        nullptr, 0, 0};
+    const float c = (float)(1.44269504088896340736 / (double)tau);
+    const DistillArgs a{logits, n, V, stride, ids, scores, k, tau, 1.0f / tau, c, weight, loss, grad, grad_stride,
+                        nullptr, nullptr, 0, 0};
     return dtype == AH_F32 ? launch<float>(a, ws, stream) : launch<uint16_t>(a, ws, stream);
 }
 

@@ -112,3 +112,28 @@ def test_grouped_starts_out_of_order_walk_no_more_tiles_than_rows_have(gpu):
     off = torch.arange(L + 1, device="cuda", dtype=torch.int64) * (T // L)
     y = ah.ah_grouped_matmul(x, mats, off, out_dtype=torch.float32)
     assert (y == w).all()
+
+
+# --------------------------------------------------------------------------- distillation: the exponents' scale
+@pytest.mark.parametrize("tau", [1.5625, 3.875, 6.6875])
+@pytest.mark.parametrize("V", [4000, 100003])
+def test_distillation_scales_exponents_by_the_nearest_factor(gpu, tau, V):
+    """q_v = 2^((z_v - M) c) with c = log2(e) / tau: an error d of c turns a small q_v by x ln2 d, x the exponent.
+    Over many values the other roundings average out, so the mean shows d: that of the float32 nearest to log2(e) / tau
+    (a quarter of 2^-24 covers the mean's own error: the factors 1 / s and tau add at most 2^-23 over exponents of 57
+    and more)."""
+    import numpy as np
+    torch, ah = gpu
+    n = 20
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    z = -tau * (40 + 40 * torch.rand(n, V, device="cuda", generator=g))
+    z[:, 0] = 0
+    ids = torch.zeros(n, 1, device="cuda", dtype=torch.int32)
+    _, grad = ah.ah_distill_topk(z, ids, torch.zeros(n, 1, device="cuda"), tau=tau)
+    far = z[:, 1:].double() / tau
+    s = 1 + far.exp().sum(1, keepdim=True)
+    rel = grad[:, 1:].double() / (tau * far.exp() / s) - 1
+    exact = np.log2(np.e) / tau
+    d = float(np.float32(exact)) / exact - 1
+    assert abs(float((rel / far).mean()) - d) <= 0.25 * 2.0 ** -24
