@@ -165,3 +165,36 @@ def test_step_without_a_row(gpu):
     loss, dx = head.step(hidden[:0], items, torch.empty((0, 5), dtype=torch.int32, device="cuda"),
                          torch.empty((0, 5), device="cuda"), want_dx=True)
     assert loss.shape == (0,) and dx.shape == (0, 64) and torch.equal(head.weights, before)
+
+
+def test_a_head_learns_from_an_index(gpu):
+    """The whole way: a partitioned index answers the teacher's queries, its leaves' centroids route the head, and the
+    head's own queries, put to the same index, come to find what the teacher's found."""
+    import numpy as np
+    import synth
+    from mips_ah_partition_amd import index as ixm
+    from mips_ah_partition_amd.search import AHIndex
+    torch, ah, qh = gpu
+    w = synth.WORKLOADS["tiny"]
+    n, m = 4000, 300
+    X = synth.rows(w, 0, n)
+    d = X.shape[1]
+    host = ixm.build(X, w.dpb, w.eta, num_leaves=16, seed=1, iters=4)
+    idx = AHIndex(host, X, num_leaves_to_search=8, reorder=100, final_num_neighbors=20)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    head = qh.QueryHead(rnd(d, 96) * 96 ** -0.5, idx.centroids, d, fan=3, seed=1)
+    hidden = rnd(m, 96).bfloat16()
+    feats = ah.ah_i8_linear(hidden, head.trunk8, head.trunk_scale, out_dtype=torch.float32)
+    ids, scores = idx.search_batched(torch.mm(feats, rnd(d, d) * d ** -0.5).contiguous())
+    items = qh.Items(torch.from_numpy(np.ascontiguousarray(X)).cuda())
+
+    def found():
+        own, _ = idx.search_batched(head.queries(hidden).contiguous())
+        return float((own[:, :, None] == ids[:, None, :]).any(2).float().mean())
+
+    before, losses = found(), []
+    for _ in range(41):
+        losses.append(float(head.step(hidden, items, ids, scores, lr=4.0)[0].mean()))
+    assert losses[-1] < 0.7 * losses[0] and found() > before + 0.05
