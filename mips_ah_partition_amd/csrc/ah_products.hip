@@ -172,11 +172,13 @@ __device__ __forceinline__ uint32_t bf16_bits(float f) {  // round to nearest ev
 //   bfloat16  the column side's fragments are read so that two of them give a lane eight
 //             consecutive columns (PERM; not by column): a store is 16 rows x 64 bytes
 //   float32   16 rows at a time, all columns (NP = 2: half of them), are turned around in LDS, rows
-//             16 bytes further apart than they are long, and stored in that order
+//             16 bytes further apart than they are long, and stored in that order (two conflicts an
+//             access by the counters, of about 128 accesses a tile and wave; operand reads have none)
 // Where rows are made of whole 64-byte sectors the stores bypass the caches' reuse order: the
 // results are not read here, and kept as others they push operands out of L2 (int8 to bfloat16,
 // 8192 x 4096 x 16384: 600 us without, 529 with).  Rows at other pitches share sectors and are
 // merged in L2 (float32, 1000 x 1536 x 100003: 424 us bypassing, 270 not).
+
 // A value that the compiler takes as new at this place: what is computed from it is not moved out of the
 // loop over tiles, where it would hold registers that the matrix loop needs.
 __device__ __forceinline__ int here(int v) {
@@ -379,9 +381,9 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // 4 x 4 (256 x 256, all accumulation registers, one wave a SIMD) loads 64 KB for 512 matrix
 // instructions, 3 x 4 an eighth more and 2 x 2 (two workgroups a CU) twice that for each of
 // them; tile_shape below chooses.
-// Measured: int8 8192 x 4096 x 16384 480 us (2.29 POP/s) of a 497-520 us call; 1000 x 1536 x 100003 to float32
-// 257 us (400 MB of outputs at an odd pitch); bfloat16 32,768 rows of 64 leaves, 1536 -> 4096, 520 us (793
-// TFLOP/s); 16,384 rows of 16 leaves, 1536 x 1536: dx 114 us, dw 175.  Bound by the power limit and by the
+// Measured: int8 8192 x 4096 x 16384 463-528 us (2.08-2.37 POP/s) of a 484-557 us call; 1000 x 1536 x 100003 to
+// float32 256-264 us (400 MB of outputs); bfloat16 32,768 rows of 64 leaves, 1536 -> 4096, 523-589 us (700-790
+// TFLOP/s); 16,384 rows of 16 leaves, 1536 x 1536: dx 110-127 us, dw 155-163.  Bound by the power limit and by the
 // step's LDS reads: a loop of these matrix instructions alone holds 1.97 GHz on random values (1935 bfloat16
 // TFLOP/s; zeros 2.40 GHz), with the LDS reads of a step 1661; the int8 kernel runs at 1.9 GHz, the bfloat16
 // one at 1.4 to 1.6.  Without the loads, the barrier or the wait for them (8192 x 6144 x 4096, bfloat16) 360, 422
@@ -868,8 +870,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
 // Tokens to int8 codes: step = max |x| / 127 (float32), code = rint(x / step), the division IEEE.
 // A row with a NaN or an infinity gets step NaN and zero codes, so that it spoils its own
-// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out; bfloat16 8192 x 4096: 23 us, 4.4 TB/s): one wave
-// per row, no barrier; the row
+// outputs and no others.  HBM-bound (2 or 4 bytes in, 1 out; bfloat16 8192 x 4096: 23 us, 4.3 TB/s; float32
+// 40 us, 4.2): one wave per row, no barrier; the row
 // is read once and kept in registers up to 8 chunks of 16 bytes a lane.  WHOLE: the rows are
 // whole aligned chunks; else chunks at any alignment, the last one short.
 template <typename T>
@@ -896,7 +898,7 @@ __device__ __forceinline__ float chunk_max(v4i v) {
     return bad ? INFINITY : m;
 }
 // rint(x / s) for the elements of a chunk.  With inv = 1 / s, t = x inv is off from the quotient by less than
-// 2e-5 (|x / s| <= 127, three roundings of 2^-24), so where t lies further than 5e-5 from the middle between
+// 2.3e-5 (|x / s| <= 127, three roundings of 2^-24), so where t lies further than 5e-5 from the middle between
 // whole numbers rint(t) is rint of the IEEE quotient; else, or where 1 / s overflows, the chunk is
 // divided (one in 600 chunks of 8).
 template <typename T>
@@ -975,7 +977,7 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(const T* x, int64_t n,
 // element, which every workgroup quantises for itself (as i8_quantize_kernel does, bit for bit).
 // HBM-bound in the weights where they are many: 64 slots of 64 leaves, 1536 x 1536, 189 MB of weights
 // in 34 us for grouping and product (5.6 TB/s); one token, 1536 -> 4096, 9.5 us a call, a launch's
-// latency (15.6 with tiles and quantising in a launch of its own).
+// latency (7.0 on the GPU; 15.6 with tiles and quantising in a launch of its own).
 constexpr int kRowWaves = 8;
 template <int MODE, int FR, bool WHOLE, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {

@@ -36,8 +36,8 @@ class QueryHead:
         self._kept = None
 
     def queries(self, hidden: torch.Tensor, keep: bool = False) -> torch.Tensor:
-        """Queries float32 [m, dim] of hidden states (bfloat16 or float32 [m, h]); keep: hold what
-        `step` needs of this forward pass."""
+        """Queries float32 [m, dim] of hidden states (bfloat16 or float32 [m, h]); keep: hold this
+        pass's features, order and gates."""
         q, x, _, offsets, order, gate, _ = self._forward(hidden)
         if keep:
             self._kept = (x, offsets, order, gate)
