@@ -375,7 +375,8 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 //                           G + 1, starts the loads of step G + 2 into step G's buffer
 // so matrix instructions run through both halves with the LDS reads and the loads issued
 // between them.  The steps of a workgroup's tiles form one sequence, so that a tile's
-// end costs its stores and nothing else: three cursors walk it, for what is multiplied, what is
+// end costs its stores and nothing else (with more than 254 leaves also its owner's walk over a run of leaf
+// starts, find): three cursors walk it, for what is multiplied, what is
 // loaded two steps ahead, and the order (rows to gather) three steps ahead.  A tile
 // has two steps at least (further ones than its sum has are zeros).
 // 4 x 4 (256 x 256, all accumulation registers, one wave a SIMD) loads 64 KB for 512 matrix
