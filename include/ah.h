@@ -52,6 +52,8 @@ enum {
 };
 
 enum { AH_F32 = 0, AH_BF16 = 1 };
+enum { AH_E4M3 = 0, AH_E5M2 = 1 };          /* 8-bit floats (OCP: no infinities in e4m3) */
+enum { AH_SILU = 0, AH_GELU = 1, AH_RELU = 2 }; /* activations; gelu is the exact one (erf) */
 
 /* Limits (AH_ERR_UNSUPPORTED beyond them). */
 #define AH_MAX_BLOCKS 4096   /* B */
@@ -517,6 +519,93 @@ size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k);
 int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
                     const float* scores, int32_t k, float tau, const float* row_weight, float* loss_out,
                     void* grad_out, int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward by leaf: in place of one matrix, every leaf has a block
+ *   h = keep * act(W_gate x) * (W_up x) / (1 - p'),   y = W_out h,
+ * where y is ah_grouped_matmul of h (fan 1).  Slots, offsets and order are those of
+ * the products above; offsets may be NULL with L == 1: every row is that leaf's.
+ *
+ * ah_grouped_gated: both projections, activation, product and dropout in one kernel.
+ *   x   bf16 [slots / fan] rows of k, x_stride apart;  w bf16 [L][2n][k], a leaf's n gate rows, then its n up rows
+ *   act AH_SILU, AH_GELU or AH_RELU
+ *   drop, seed, step: dropout of h as in ah_dropout, row = slot, column in [0, n); drop 0: none
+ *   pre_out bf16 [slots][2n] the two projections (gate, up), or NULL: what the backward pass needs
+ *   out [slots][n] of out_dtype: h.  Rows of no leaf are zero in both.
+ * h is computed from the float32 sums and rounded once; pre_out is rounded to bf16.
+ * ah_grouped_gated_grad: from the gradient of y to those of the projections, in one kernel.  With dh = W_out^T dy
+ * (float32, not stored), a and b from pre, keep and p' as in the forward call:
+ *   dpre_out[s] = (dh b act'(a), dh act(a)) keep / (1 - p'),   hidden_out[s] = h
+ *   dy  bf16 [slots] rows of d, dy_stride apart;  w bf16 [L][d][n] (W_out);  pre bf16 [slots][2n]
+ *   dpre_out bf16 [slots][2n]; may be pre itself;  hidden_out bf16 [slots][n] or NULL.  Rows of no leaf are zero.
+ * With these the remaining gradients are the products': dx = ah_grouped_matmul_dx(dpre, W) (n there = 2n here),
+ * dW = ah_grouped_matmul_dw(dpre, x), dW_out = ah_grouped_matmul_dw(dy, hidden).
+ * Sums are float32 in a fixed order.  relu has the derivative 0 at 0.  A dropped element is 0 whatever it was (a
+ * NaN or an infinity too), and so are its gradients.
+ * Errors: those of ah_grouped_matmul; AH_ERR_SHAPE (drop outside [0, 1)), AH_ERR_UNSUPPORTED (act, n >
+ * AH_MAX_WIDTH / 2, step not 8-byte aligned), AH_ERR_NULL (offsets NULL with L > 1).
+ */
+int ah_grouped_gated(const void* x, int64_t x_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                     const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, int32_t act, double drop,
+                     uint64_t seed, const int64_t* step, void* pre_out, void* out, int32_t out_dtype, void* stream);
+int ah_grouped_gated_grad(const void* dy, int64_t dy_stride, const void* w, int32_t L, int32_t d, int32_t n,
+                          const int64_t* offsets, const int32_t* order, int64_t slots, const void* pre, int32_t act,
+                          double drop, uint64_t seed, const int64_t* step, void* dpre_out, void* hidden_out,
+                          void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit floating point (AH_E4M3, AH_E5M2) with a power-of-two scale for each
+ * block of 128 along the sum, which the matrix instruction applies itself.
+ *
+ * A matrix of n rows and d summed columns is held as
+ *   codes uint8 [n][kp], kp = d rounded up to a multiple of 128, zeros past d
+ *   scale uint8 [kp / 128][np], np = n rounded up to a multiple of 16: byte e + 127 of row r, block b at [b][r]
+ * and stands for code * 2^e.  Both 16-byte aligned.
+ * ah_f8_quantize: e is the smallest (from -127 on) with max |x| 2^-e over the block at most the type's largest value
+ * (448, 57344): nothing is clipped; the codes are x 2^-e rounded to nearest even.  A block of zeros has e = 0; one
+ * with a NaN or an infinity has e = 0 and NaN codes (0x7F): its row's products are NaN, other rows' are not touched.
+ *   x [n] rows of d elements, x_stride apart
+ *   codes_out, scale_out      of x, blocks along d; or NULL
+ *   codes_t_out, scale_t_out  of x transposed: [d] rows, blocks along n; or NULL (the operands of a weight
+ *                             gradient dy^T x, and of dx = dy w from w's columns)
+ * ah_f8_matmul: out[i][j] = sum over the blocks of 2^(ex + ew) (x8_i . w8_j) (+ bias[j]), rounded once to out's type.
+ * Accumulated in float32; inside, the matrix instruction cuts the products of each eight elements off at 2^-13 of
+ * the power of two below the largest of them: where float32 results need more than about 1e-5 of their size, use
+ * the bfloat16 products.
+ *   x8, x_scale: m rows;  w8, w_scale: n rows;  k the summed length, the same for both;  bias float32 [n] or NULL;
+ *   out [m][n]
+ * ah_f8_linear: ah_f8_quantize of x, then ah_f8_matmul, the same results.
+ *   workspace >= ah_f8_linear_workspace_bytes(m, k) bytes, 16-byte aligned
+ * Errors: AH_ERR_SHAPE (m, n < 0, k or d < 1, x_stride below the row), AH_ERR_UNSUPPORTED (a dtype, k or d >
+ * AH_MAX_WIDTH, m or n > 2^30, n > AH_MAX_WIDTH with codes_t_out, a pointer not aligned), AH_ERR_NULL,
+ * AH_ERR_WORKSPACE.  m == 0 or n == 0 is a successful no-op.
+ */
+int ah_f8_quantize(const void* x, int32_t x_dtype, int64_t n, int64_t d, int64_t x_stride, int32_t type,
+                   uint8_t* codes_out, uint8_t* scale_out, uint8_t* codes_t_out, uint8_t* scale_t_out, void* stream);
+int ah_f8_matmul(const uint8_t* x8, const uint8_t* x_scale, int32_t x_type, int64_t m, const uint8_t* w8,
+                 const uint8_t* w_scale, int32_t w_type, int64_t n, int64_t k, const float* bias, void* out,
+                 int32_t out_dtype, void* stream);
+size_t ah_f8_linear_workspace_bytes(int64_t m, int64_t k);
+int ah_f8_linear(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t x_stride, int32_t x_type,
+                 const uint8_t* w8, const uint8_t* w_scale, int32_t w_type, int64_t n, const float* bias, void* out,
+                 int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout with a mask that is computed and never stored:
+ *   out = keep * x / (1 - p') (+ residual)
+ * keep[r][c] = (u >= t), t = rint(65536 p), p' = t / 65536, with u the c % 8-th 16 bits (low halves first) of
+ * Philox4x32-10 at the key seed and the counter (c / 8, r, step): a function of seed, step, row and column alone.
+ * The gradient is the same call on the output's gradient, without the residual.
+ *   x, residual (or NULL), out: rows of n elements of dtype, their strides apart; out may be x or residual
+ *   p in [0, 1);  step int64 on the device (read when the kernel runs: a captured graph gets new masks by
+ *   counting it up), or NULL = 0
+ * A dropped element is 0 whatever it was.  Float32 arithmetic, rounded once.
+ * Errors: AH_ERR_SHAPE (rows < 0, n < 1, a stride < n, p outside [0, 1)), AH_ERR_UNSUPPORTED (dtype, rows or n >=
+ * 2^31, step not 8-byte aligned), AH_ERR_NULL.
+ */
+int ah_dropout(const void* x, int32_t dtype, int64_t rows, int64_t n, int64_t x_stride, double p, uint64_t seed,
+               const int64_t* step, const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+               void* stream);
 
 #ifdef __cplusplus
 }

@@ -41,6 +41,9 @@ EXPORTS = (
     "ah_group_rows_workspace_bytes", "ah_group_rows", "ah_grouped_matmul",
     "ah_grouped_dx_workspace_bytes", "ah_grouped_matmul_dx", "ah_grouped_matmul_dw",
     "ah_distill_workspace_bytes", "ah_distill_topk",
+    "ah_grouped_gated", "ah_grouped_gated_grad",
+    "ah_f8_quantize", "ah_f8_matmul", "ah_f8_linear_workspace_bytes", "ah_f8_linear",
+    "ah_dropout",
 )
 # every symbol include/ah_instrument.h declares (measurement hooks)
 INSTRUMENT_EXPORTS = ("ah_scan_topk_timed", "ah_scan_workspace_counters", "ah_hbm_read_probe")
@@ -141,6 +144,21 @@ def lib() -> C.CDLL:
         L.ah_distill_workspace_bytes.argtypes = [i64, i64, i32]
         L.ah_distill_topk.restype = C.c_int
         L.ah_distill_topk.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, vp, vp, vp, i64, vp, sz, vp]
+        u64, f64 = C.c_uint64, C.c_double
+        L.ah_grouped_gated.restype = C.c_int
+        L.ah_grouped_gated.argtypes = [vp, i64, vp, i32, i32, i32, vp, vp, i64, i32, i32, f64, u64, vp, vp, vp, i32, vp]
+        L.ah_grouped_gated_grad.restype = C.c_int
+        L.ah_grouped_gated_grad.argtypes = [vp, i64, vp, i32, i32, i32, vp, vp, i64, vp, i32, f64, u64, vp, vp, vp, vp]
+        L.ah_f8_quantize.restype = C.c_int
+        L.ah_f8_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp]
+        L.ah_f8_matmul.restype = C.c_int
+        L.ah_f8_matmul.argtypes = [vp, vp, i32, i64, vp, vp, i32, i64, i64, vp, vp, i32, vp]
+        L.ah_f8_linear_workspace_bytes.restype = sz
+        L.ah_f8_linear_workspace_bytes.argtypes = [i64, i64]
+        L.ah_f8_linear.restype = C.c_int
+        L.ah_f8_linear.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, i32, i64, vp, vp, i32, vp, sz, vp]
+        L.ah_dropout.restype = C.c_int
+        L.ah_dropout.argtypes = [vp, i32, i64, i64, i64, f64, u64, vp, vp, i64, vp, i64, vp]
         L.ah_scan_topk_noalloc.restype = C.c_int
         L.ah_scan_topk_noalloc.argtypes = [vp, i64, i32, vp, i32, i64, vp, vp, i32, vp, i32, i32, vp, vp, vp]
         L.ah_scan_workspace_counters.restype = C.c_int
@@ -853,6 +871,219 @@ def ah_distill_topk(logits, ids, scores, tau=1.0, row_weight=None, want_grad=Tru
                                  _at(row_weight), _at(loss_out), _at(grad_out), gs, _at(workspace),
                                  _nbytes(workspace), _on(stream, logits)), "ah_distill_topk")
     return loss_out, grad_out
+
+
+# ----------------------------------------------------------------------------- gated blocks, 8-bit floats, dropout
+_ACTS = {"silu": 0, "gelu": 1, "relu": 2}
+_F8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+
+
+def _call(name, where, *args):
+    """One library call with `where`'s device current, whatever device is."""
+    dev = where.get_device()
+    if dev == torch._C._cuda_getDevice():
+        status = getattr(lib(), name)(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), name)(*args)
+    _check(status, name)
+
+
+def _together(where, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != where.get_device():
+            raise ValueError(f"{name} is on another device")
+
+
+def _act_code(act):
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return code
+
+
+def _count(step):
+    if step is not None and _is(step, torch.int64, "step", step.dim() if isinstance(step, torch.Tensor) else 1).numel() != 1:
+        raise ValueError("step must be one int64")
+    return step
+
+
+def _leaf_starts(offsets, order, fan, slots, L):
+    if offsets is not None:
+        _groups(offsets, order, fan, slots, L)
+    elif L != 1 or order is not None or fan != 1:
+        raise ValueError("rows without offsets belong to one leaf, without an order or a fan")
+
+
+def ah_grouped_gated(x, w, offsets=None, order=None, fan=1, act="silu", drop=0.0, seed=0, step=None, want_pre=False,
+                     out_dtype=torch.bfloat16, out=None, pre_out=None, stream=None):
+    """h[s] = act(gate) * up of slot s's leaf, with dropout: x bfloat16 [m, k], w bfloat16 [L, 2n, k] (gate rows, then
+    up rows), offsets and order as from ah_group_rows (none: one leaf has every row).  Returns (h [m * fan, n],
+    the projections bfloat16 [m * fan, 2n] for the backward pass with want_pre, else None)."""
+    x, xs = _rows(x, torch.bfloat16, "x")
+    _is(w, torch.bfloat16, "w", 3)
+    m, k = x.shape
+    L, n2, kw = w.shape
+    if kw != k or n2 % 2:
+        raise ValueError("w needs two rows of x's width for each output column")
+    slots, n = m * fan, n2 // 2
+    _leaf_starts(offsets, order, fan, slots, L)
+    _count(step)
+    _together(x, w=w, offsets=offsets, order=order, step=step, out=out, pre_out=pre_out)
+    dtype = out_dtype if out is None else out.dtype
+    odt = _float_code(dtype, "out")
+    out = _out(out, (slots, n), dtype, "out", x.device, stream)
+    if pre_out is not None or want_pre:
+        pre_out = _out(pre_out, (slots, n2), torch.bfloat16, "pre_out", x.device, stream)
+    _call("ah_grouped_gated", x, _at(x), xs, _at(w), L, n, k, _at(offsets), _at(order), slots, fan, _act_code(act),
+          float(drop), int(seed) & (2 ** 64 - 1), _at(step), _at(pre_out), _at(out), odt, _on(stream, x))
+    return out, pre_out
+
+
+def ah_grouped_gated_grad(dy, w, pre, offsets=None, order=None, act="silu", drop=0.0, seed=0, step=None,
+                          want_hidden=True, dpre_out=None, hidden_out=None, stream=None):
+    """From the gradient of a gated block's output to its projections': dy bfloat16 [slots, d], w bfloat16 [L, d, n] (the
+    output layer), pre bfloat16 [slots, 2n] and the dropout's arguments as in the forward call.  Returns (dpre bfloat16
+    [slots, 2n], h bfloat16 [slots, n] computed again for the output layer's gradient, or None)."""
+    dy, dys = _rows(dy, torch.bfloat16, "dy")
+    _is(w, torch.bfloat16, "w", 3)
+    _is(pre, torch.bfloat16, "pre", 2)
+    slots, d = dy.shape
+    L, dw, n = w.shape
+    if dw != d or tuple(pre.shape) != (slots, 2 * n):
+        raise ValueError("w and pre must have the widths of dy and of the block")
+    _leaf_starts(offsets, order, 1, slots, L)
+    _count(step)
+    _together(dy, w=w, pre=pre, offsets=offsets, order=order, step=step, dpre_out=dpre_out, hidden_out=hidden_out)
+    dpre_out = _out(dpre_out, (slots, 2 * n), torch.bfloat16, "dpre_out", dy.device, stream)
+    if hidden_out is not None or want_hidden:
+        hidden_out = _out(hidden_out, (slots, n), torch.bfloat16, "hidden_out", dy.device, stream)
+    _call("ah_grouped_gated_grad", dy, _at(dy), dys, _at(w), L, d, n, _at(offsets), _at(order), slots, _at(pre),
+          _act_code(act), float(drop), int(seed) & (2 ** 64 - 1), _at(step), _at(dpre_out), _at(hidden_out),
+          _on(stream, dy))
+    return dpre_out, hidden_out
+
+
+def _f8_code(dtype, name):
+    code = _F8.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2, got {dtype}")
+    return code
+
+
+def _f8_shapes(n, d):
+    """Shapes of the codes and of the scales of n rows of d."""
+    kb = (d + 127) // 128
+    return (n, kb * 128), (kb, (n + 15) // 16 * 16)
+
+
+def ah_f8_quantize(x, dtype=torch.float8_e4m3fn, want_rows=True, want_columns=False, codes_out=None, scale_out=None,
+                   codes_t_out=None, scale_t_out=None, stream=None):
+    """8-bit codes of x (float32 or bfloat16 [n, d]) with a scale 2^(byte - 127) for each block of 128: (codes [n, d to a
+    multiple of 128], scales uint8 [blocks, n to a multiple of 16]) along the rows and, with want_columns, the
+    same of x transposed; None, None for what is not wanted."""
+    x, xs = _rows(x, None, "x")
+    dt, code = _float_code(x.dtype, "x"), _f8_code(dtype, "dtype")
+    n, d = x.shape
+    _together(x, codes_out=codes_out, scale_out=scale_out, codes_t_out=codes_t_out, scale_t_out=scale_t_out)
+    if want_rows or codes_out is not None:
+        cs, ss = _f8_shapes(n, d)
+        codes_out = _out(codes_out, cs, dtype, "codes_out", x.device, stream)
+        scale_out = _out(scale_out, ss, torch.uint8, "scale_out", x.device, stream)
+    if want_columns or codes_t_out is not None:
+        cs, ss = _f8_shapes(d, n)
+        codes_t_out = _out(codes_t_out, cs, dtype, "codes_t_out", x.device, stream)
+        scale_t_out = _out(scale_t_out, ss, torch.uint8, "scale_t_out", x.device, stream)
+    _call("ah_f8_quantize", x, _at(x), dt, n, d, xs, code, _at(codes_out), _at(scale_out), _at(codes_t_out),
+          _at(scale_t_out), _on(stream, x))
+    return codes_out, scale_out, codes_t_out, scale_t_out
+
+
+def _f8_operand(codes, scale, name):
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError(f"{name} must be a device tensor")
+    code = _f8_code(codes.dtype, name)
+    _is(codes, codes.dtype, name, 2)
+    _is(scale, torch.uint8, f"{name}'s scale", 2)
+    n, kp = codes.shape
+    if kp % 128 or tuple(scale.shape) != _f8_shapes(n, kp)[1]:
+        raise ValueError(f"{name} and its scale must have the shapes that ah_f8_quantize gives")
+    return code, n, kp
+
+
+def _f8_bias(bias, n):
+    if bias is not None and _is(bias, torch.float32, "bias", 1).numel() != n:
+        raise ValueError("bias needs one entry for each output column")
+
+
+def ah_f8_matmul(x8, x_scale, w8, w_scale, bias=None, out_dtype=torch.bfloat16, out=None, stream=None):
+    """What the rows of x8 and of w8 stand for, multiplied: out [m, n] (+ bias).  Codes and scales as ah_f8_quantize
+    makes them."""
+    xc, m, k = _f8_operand(x8, x_scale, "x8")
+    wc, n, kw = _f8_operand(w8, w_scale, "w8")
+    if kw != k:
+        raise ValueError("w8 and x8 differ in their width")
+    _f8_bias(bias, n)
+    _together(x8, x_scale=x_scale, w8=w8, w_scale=w_scale, bias=bias, out=out)
+    dtype = out_dtype if out is None else out.dtype
+    odt = _float_code(dtype, "out")
+    out = _out(out, (m, n), dtype, "out", x8.device, stream)
+    if k == 0:  # a sum over nothing
+        with torch.cuda.stream(stream):
+            return out.zero_() if bias is None else out.copy_(bias.expand(m, n))
+    _call("ah_f8_matmul", x8, _at(x8), _at(x_scale), xc, m, _at(w8), _at(w_scale), wc, n, k, _at(bias), _at(out), odt,
+          _on(stream, x8))
+    return out
+
+
+def ah_f8_linear_workspace_bytes(m: int, k: int) -> int:
+    return int(lib().ah_f8_linear_workspace_bytes(m, k))
+
+
+def ah_f8_linear(x, w8, w_scale, bias=None, x_type=torch.float8_e4m3fn, out_dtype=torch.bfloat16, out=None,
+                 workspace=None, stream=None):
+    """A linear layer in 8-bit floats: the rows of x (float32 or bfloat16 [m, k]) quantised to x_type, times w8
+    (ah_f8_quantize of weights [n, k])."""
+    x, xs = _rows(x, None, "x")
+    dt, xc = _float_code(x.dtype, "x"), _f8_code(x_type, "x_type")
+    m, k = x.shape
+    wc, n, kw = _f8_operand(w8, w_scale, "w8")
+    if kw != (k + 127) // 128 * 128:
+        raise ValueError("w8 and x differ in their width")
+    _f8_bias(bias, n)
+    _together(x, w8=w8, w_scale=w_scale, bias=bias, out=out, workspace=workspace)
+    dtype = out_dtype if out is None else out.dtype
+    odt = _float_code(dtype, "out")
+    out = _out(out, (m, n), dtype, "out", x.device, stream)
+    workspace = _work(workspace, ah_f8_linear_workspace_bytes(m, k), "workspace", x.device, stream)
+    _call("ah_f8_linear", x, _at(x), dt, m, k, xs, xc, _at(w8), _at(w_scale), wc, n, _at(bias), _at(out), odt,
+          _at(workspace), _nbytes(workspace), _on(stream, x))
+    return out
+
+
+def ah_dropout(x, p, seed, step=None, residual=None, out=None, stream=None):
+    """x with each element dropped with probability p and the others multiplied by 1 / (1 - p) (+ residual): float32 or
+    bfloat16 [rows, n].  The mask is a function of seed, step (int64 on the device, none: 0), row and column;
+    the gradient is the same call on the output's gradient."""
+    x, xs = _rows(x, None, "x")
+    dt = _float_code(x.dtype, "x")
+    rows, n = x.shape
+    rs = os_ = n
+    if residual is not None:
+        residual, rs = _rows(residual, x.dtype, "residual")
+        if residual.shape != x.shape:
+            raise ValueError("residual must have the shape of x")
+    if out is None:
+        out = _empty((rows, n), x.dtype, x.device, stream)
+    else:
+        out, os_ = _rows(out, x.dtype, "out")
+        if out.shape != x.shape:
+            raise ValueError("out must have the shape of x")
+    _count(step)
+    _together(x, step=step, residual=residual, out=out)
+    _call("ah_dropout", x, _at(x), dt, rows, n, xs, float(p), int(seed) & (2 ** 64 - 1), _at(step), _at(residual), rs,
+          _at(out), os_, _on(stream, x))
+    return out
 
 
 # ----------------------------------------------------------------------------- measurement hooks

@@ -4,6 +4,7 @@
 #include "../../include/ah.h"
 #include "../../include/ah_instrument.h"
 #include "ah_kernels.hpp"
+#include "ah_random.hpp"
 
 #include <mutex>
 
@@ -479,6 +480,108 @@ int ah_grouped_matmul_dw(const void* dy, int64_t dy_stride, const void* x, int64
     if ((slots > 0 && (!dy || !x)) || !offsets || !dw_out) return AH_ERR_NULL;
     const ah::GroupedProblem g{x, x_stride, dy, dy_stride, nullptr, L, n, k, offsets, order, slots, fan};
     return hip_status(ah::launch_grouped_dw(g, dw_out, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+// What gated products share beyond grouped_check.
+static int gated_check(int32_t act, double drop, const int64_t* step, int32_t L, int32_t n, const int64_t* offsets,
+                       const int32_t* order, int32_t fan) {
+    if (!(drop >= 0.0) || !(drop < 1.0) || (!order && fan != 1)) return AH_ERR_SHAPE;
+    if (act < AH_SILU || act > AH_RELU || n > AH_MAX_WIDTH / 2 || (reinterpret_cast<uintptr_t>(step) & 7) != 0)
+        return AH_ERR_UNSUPPORTED;
+    return !offsets && L != 1 ? AH_ERR_NULL : AH_OK;
+}
+
+int ah_grouped_gated(const void* x, int64_t x_stride, const void* w, int32_t L, int32_t n, int32_t k,
+                     const int64_t* offsets, const int32_t* order, int64_t slots, int32_t fan, int32_t act, double drop,
+                     uint64_t seed, const int64_t* step, void* pre_out, void* out, int32_t out_dtype, void* stream) {
+    int chk = grouped_check(slots, fan, L, n, k, x_stride, k, out_dtype);
+    if (chk != AH_OK || slots == 0) return chk;
+    chk = gated_check(act, drop, step, L, n, offsets, order, fan);
+    if (chk != AH_OK) return chk;
+    if (!x || !w || !out) return AH_ERR_NULL;
+    const ah::GatedProblem g{x, x_stride, w, L, n, k, offsets, order, slots, fan};
+    return hip_status(ah::launch_gated(g, ah::make_dropout(drop, seed, step), act, pre_out, out, out_dtype,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+int ah_grouped_gated_grad(const void* dy, int64_t dy_stride, const void* w, int32_t L, int32_t d, int32_t n,
+                          const int64_t* offsets, const int32_t* order, int64_t slots, const void* pre, int32_t act,
+                          double drop, uint64_t seed, const int64_t* step, void* dpre_out, void* hidden_out,
+                          void* stream) {
+    int chk = grouped_check(slots, 1, L, n, d, dy_stride, d, AH_BF16);
+    if (chk != AH_OK || slots == 0) return chk;
+    chk = gated_check(act, drop, step, L, n, offsets, order, 1);
+    if (chk != AH_OK) return chk;
+    if (!dy || !w || !pre || !dpre_out) return AH_ERR_NULL;
+    const ah::GatedProblem g{dy, dy_stride, w, L, n, d, offsets, order, slots, 1};
+    return hip_status(ah::launch_gated_grad(g, ah::make_dropout(drop, seed, step), act, pre, dpre_out, hidden_out,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+static inline bool f8_type(int32_t t) { return t == AH_E4M3 || t == AH_E5M2; }
+
+int ah_f8_quantize(const void* x, int32_t x_dtype, int64_t n, int64_t d, int64_t x_stride, int32_t type,
+                   uint8_t* codes_out, uint8_t* scale_out, uint8_t* codes_t_out, uint8_t* scale_t_out, void* stream) {
+    if (n < 0 || d < 1 || x_stride < d) return AH_ERR_SHAPE;
+    if (!float_type(x_dtype) || !f8_type(type) || d > AH_MAX_WIDTH || n > ((int64_t)1 << 30) ||
+        (codes_t_out && n > AH_MAX_WIDTH))
+        return AH_ERR_UNSUPPORTED;
+    if (n == 0) return AH_OK;
+    if (!x || (!codes_out && !codes_t_out) || (codes_out && !scale_out) || (codes_t_out && !scale_t_out))
+        return AH_ERR_NULL;
+    if (!a16(codes_out) || !a16(scale_out) || !a16(codes_t_out) || !a16(scale_t_out)) return AH_ERR_UNSUPPORTED;
+    return hip_status(ah::launch_f8_quantize(x, x_dtype, n, d, x_stride, type, codes_out, scale_out, codes_t_out,
+                                             scale_t_out, static_cast<hipStream_t>(stream)));
+}
+
+int ah_f8_matmul(const uint8_t* x8, const uint8_t* x_scale, int32_t x_type, int64_t m, const uint8_t* w8,
+                 const uint8_t* w_scale, int32_t w_type, int64_t n, int64_t k, const float* bias, void* out,
+                 int32_t out_dtype, void* stream) {
+    if (m < 0 || n < 0 || k < 1) return AH_ERR_SHAPE;
+    if (!f8_type(x_type) || !f8_type(w_type) || !float_type(out_dtype) || k > AH_MAX_WIDTH ||
+        m > ((int64_t)1 << 30) || n > ((int64_t)1 << 30))
+        return AH_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return AH_OK;
+    if (!x8 || !x_scale || !w8 || !w_scale || !out) return AH_ERR_NULL;
+    if (!a16(x8) || !a16(x_scale) || !a16(w8) || !a16(w_scale)) return AH_ERR_UNSUPPORTED;
+    const ah::F8Problem g{x8, x_scale, w8, w_scale, x_type, w_type, m, n, k};
+    return hip_status(ah::launch_f8_matmul(g, bias, out, out_dtype, static_cast<hipStream_t>(stream)));
+}
+
+size_t ah_f8_linear_workspace_bytes(int64_t m, int64_t k) {
+    if (m < 0 || k < 1) return 0;
+    return ah::f8_linear_workspace_bytes(m, k);
+}
+
+int ah_f8_linear(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t x_stride, int32_t x_type,
+                 const uint8_t* w8, const uint8_t* w_scale, int32_t w_type, int64_t n, const float* bias, void* out,
+                 int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (m < 0 || n < 0 || k < 1 || x_stride < k) return AH_ERR_SHAPE;
+    if (!float_type(x_dtype) || !f8_type(x_type) || !f8_type(w_type) || !float_type(out_dtype) ||
+        k > AH_MAX_WIDTH || m > ((int64_t)1 << 30) || n > ((int64_t)1 << 30))
+        return AH_ERR_UNSUPPORTED;
+    if (m == 0 || n == 0) return AH_OK;
+    if (!x || !w8 || !w_scale || !out) return AH_ERR_NULL;
+    if (!workspace || workspace_bytes < ah::f8_linear_workspace_bytes(m, k)) return AH_ERR_WORKSPACE;
+    if (!a16(workspace) || !a16(w8) || !a16(w_scale)) return AH_ERR_UNSUPPORTED;
+    const ah::F8Problem g{nullptr, nullptr, w8, w_scale, x_type, w_type, m, n, k};
+    return hip_status(ah::launch_f8_linear(x, x_dtype, x_stride, g, bias, out, out_dtype, workspace,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+int ah_dropout(const void* x, int32_t dtype, int64_t rows, int64_t n, int64_t x_stride, double p, uint64_t seed,
+               const int64_t* step, const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+               void* stream) {
+    if (rows < 0 || n < 1 || x_stride < n || out_stride < n || (residual && residual_stride < n) || !(p >= 0.0) ||
+        !(p < 1.0))
+        return AH_ERR_SHAPE;
+    if (!float_type(dtype) || n >= ((int64_t)1 << 31) || rows >= ((int64_t)1 << 31) ||
+        (reinterpret_cast<uintptr_t>(step) & 7) != 0)
+        return AH_ERR_UNSUPPORTED;
+    if (rows == 0) return AH_OK;
+    if (!x || !out) return AH_ERR_NULL;
+    return hip_status(ah::launch_dropout(x, dtype, rows, n, x_stride, ah::make_dropout(p, seed, step), residual,
+                                         residual_stride, out, out_stride, static_cast<hipStream_t>(stream)));
 }
 
 size_t ah_distill_workspace_bytes(int64_t n, int64_t V, int32_t k) {

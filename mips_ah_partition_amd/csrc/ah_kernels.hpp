@@ -132,6 +132,40 @@ size_t grouped_dx_workspace_bytes(int64_t slots, int32_t k, int32_t fan);
 hipError_t launch_grouped_dx(const GroupedProblem& g, void* out, int32_t out_dtype, void* ws, hipStream_t stream);
 hipError_t launch_grouped_dw(const GroupedProblem& g, void* out, int32_t out_dtype, hipStream_t stream);
 
+// Gated feed-forward by leaf: the two projections with activation, product and dropout, and back.
+struct Dropout;
+struct GatedProblem {
+    const void* q;       // bf16 [slots / fan][q_stride]: x, or (gradient, fan 1) dy
+    int64_t q_stride;
+    const void* w;       // bf16 [L][2 n][k], or (gradient) [L][k][n]
+    int32_t L, n, k;     // n: the block's hidden width; k: the summed width
+    const int64_t* offsets;  // NULL: one leaf has all rows
+    const int32_t* order;
+    int64_t slots;
+    int32_t fan;
+};
+hipError_t launch_gated(const GatedProblem& g, const Dropout& d, int32_t act, void* pre, void* out, int32_t out_dtype,
+                        hipStream_t stream);
+hipError_t launch_gated_grad(const GatedProblem& g, const Dropout& d, int32_t act, const void* pre, void* dpre,
+                             void* hidden, hipStream_t stream);
+
+// 8-bit floating point with a power-of-two scale for each block of 128 along the sum.
+struct F8Problem {
+    const uint8_t *x8, *xs, *w8, *ws;
+    int32_t x_type, w_type;
+    int64_t m, n, k;
+};
+hipError_t launch_f8_quantize(const void* x, int32_t dtype, int64_t n, int64_t d, int64_t xs, int32_t type,
+                              uint8_t* codes, uint8_t* scale, uint8_t* codes_t, uint8_t* scale_t, hipStream_t stream);
+hipError_t launch_f8_matmul(const F8Problem& g, const float* bias, void* out, int32_t out_dtype, hipStream_t stream);
+size_t f8_linear_workspace_bytes(int64_t m, int64_t k);
+hipError_t launch_f8_linear(const void* x, int32_t dtype, int64_t xs, const F8Problem& g, const float* bias, void* out,
+                            int32_t out_dtype, void* work, hipStream_t stream);
+
+// Dropout by a counter-based generator, with a residual.
+hipError_t launch_dropout(const void* x, int32_t dtype, int64_t rows, int64_t n, int64_t xs, const Dropout& d,
+                          const void* res, int64_t rs, void* out, int64_t os, hipStream_t stream);
+
 // Distillation from a teacher's (ids, scores): loss and gradient.
 size_t distill_workspace_bytes(int64_t n, int64_t V, int32_t k);
 hipError_t launch_distill(const void* logits, int32_t dtype, int64_t n, int64_t V, int64_t stride, const int32_t* ids,
