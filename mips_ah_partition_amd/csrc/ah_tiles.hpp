@@ -7,6 +7,9 @@
 //   forward  Q = queries of a leaf,      P = the leaf's W [n][k]     t = k
 //   dx       Q = slot gradients,         P = the leaf's W, by column t = n
 //   dw       Q = slot gradients by column, P = queries by column     t = the leaf's rows
+//   gate     Q = queries of a leaf,      P = the leaf's gate and up rows [2n][k], in turn: a wave has both of a column
+//   grad     as dx, of a gated block's output layer
+//   float8   Q = codes [m][kp],          P = codes [n][kp]           t = kp, a scale for each row and step
 // "By column" operands have the summed index along memory rows; their LDS tiles
 // are read with the transposing LDS load (ds_read_b64_tr_b16).
 //
@@ -23,7 +26,10 @@
 // & 1) << 1).  The matrix instruction takes P as its A operand, so
 // that a lane ends with four consecutive output columns of one row.
 #pragma once
+#include <type_traits>
+
 #include "ah_device.hpp"
+#include "ah_gating.hpp"
 #include "ah_kernels.hpp"
 #include "../../include/ah.h"
 
@@ -34,7 +40,13 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef short v8s __attribute__((ext_vector_type(8)));
 
-enum { kI8 = 0, kFwd = 1, kDx = 2, kDw = 3 };
+enum { kI8 = 0, kFwd = 1, kDx = 2, kDw = 3, kGate = 4, kGrad = 5, kF8 = 8 };  // kF8 + Q's type + 2 * P's type
+constexpr bool is_f8(int mode) { return mode >= kF8; }
+constexpr bool is_plain(int mode) { return mode == kI8 || is_f8(mode); }  // one matrix, rows in order
+constexpr bool is_gated(int mode) { return mode == kGate || mode == kGrad; }
+constexpr bool is_ragged(int mode) { return !is_plain(mode) && mode != kDw; }
+constexpr bool p_by_col(int mode) { return mode == kDx || mode == kDw || mode == kGrad; }
+constexpr int elem_bytes(int mode) { return is_plain(mode) ? 1 : 2; }
 
 constexpr int kNT = 256;     // threads: 2 x 2 waves
 constexpr int kCUs = 256;    // compute units of an MI355X (a multiple of its 8 XCDs)
@@ -58,7 +70,12 @@ struct ProdArgs {
     void* out;
     int32_t out_f32;
     int32_t bypass;        // rows of whole 64-byte sectors
-    const float *sx, *sw, *bias;  // int8
+    const float *sx, *sw, *bias;  // int8 (bias: float8 too)
+    int32_t act;           // gated: activation, dropout, the projections [slots][2 J] (gate: written, or NULL; grad: read)
+    Dropout drop;          // and h (grad; or NULL)
+    char *pre, *hidden;
+    const char *qsc, *psc; // float8: scale bytes [steps][pitch]
+    int64_t qpitch, ppitch;
 };
 
 typedef const __attribute__((address_space(3))) v4i* lds_v4i;
@@ -75,6 +92,12 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // m0, which the compiler keeps nothing in, is set in the same block.
 __device__ __forceinline__ void dma16(const char* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     __builtin_amdgcn_readfirstlane(lds)),
+                 "v"(src));
+}
+// 4 bytes a lane, at lds + 4 * lane.
+__device__ __forceinline__ void dma4(const char* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(
                      __builtin_amdgcn_readfirstlane(lds)),
                  "v"(src));
 }
@@ -106,6 +129,15 @@ __device__ __forceinline__ typename Acc<MODE>::type mma(v4i p, v4i q, typename A
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, p), __builtin_bit_cast(v8bf, q), c, 0,
                                                        0, 0);
+}
+
+// 128 bytes of the sum: halves lo and hi of 64; scale bytes in the low bytes of sp and sq.
+template <int MODE>
+__device__ __forceinline__ v4f mma8(v4i plo, v4i phi, v4i qlo, v4i qhi, v4f c, int sp, int sq) {
+    const v8i p = __builtin_shufflevector(plo, phi, 0, 1, 2, 3, 4, 5, 6, 7),
+              q = __builtin_shufflevector(qlo, qhi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, (MODE - kF8) >> 1 & 1, (MODE - kF8) & 1, 0, sp, 0,
+                                                            sq);
 }
 
 // Element of an accumulator that is kept in the accumulation registers.  (All its uses but the
@@ -187,7 +219,7 @@ __device__ __forceinline__ int here(int v) {
 }
 
 template <int MODE, int OB>
-constexpr bool kPerm = OB == 2 && MODE < kDx;
+constexpr bool kPerm = OB == 2 && !p_by_col(MODE);
 template <int NP>
 constexpr int kTurnCols = NP == 2 ? 32 : 64;
 template <int NP>
@@ -240,6 +272,11 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
                 v[e] = (float)r[e] * sx * sw[e];
                 if (a.bias) v[e] += bias[e];
             }
+        } else if constexpr (is_f8(MODE)) {
+            const v4f bias = *reinterpret_cast<const v4f*>(
+                sc + c0 + (Y == 2 ? (y >> 1) * 32 + g * 8 + (y & 1) * 4 : y * 16 + g * 4));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = r[e] + bias[e];
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = r[e];
@@ -311,6 +348,148 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
     }
 }
 
+// N consecutive bfloat16 values (N of 4 or 8), of which `left` exist.
+template <int N>
+__device__ __forceinline__ void put_bf16(char* o, const float* v, int32_t left) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) w[e] = bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16;
+    if (left >= N)
+        __builtin_memcpy(o, w, 2 * N);
+    else if (left > 0)
+        store_left<2>(o, v4i{(int)w[0], (int)w[1], (int)w[N / 2 - 2], (int)w[N / 2 - 1]}, left);
+}
+template <int N>
+__device__ __forceinline__ void get_bf16(const char* p, float* v, int32_t left) {
+    uint16_t b[N] = {};
+    if (left >= N) {
+        __builtin_memcpy(b, p, 2 * N);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) __builtin_memcpy(b + e, p + 2 * e, 2);
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __uint_as_float((uint32_t)b[e] << 16);
+}
+// Factors of N (4 or 8) columns from j on (a multiple of N) of a row.
+template <int N>
+__device__ __forceinline__ void dropout_factors(const Dropout& d, uint64_t step, int32_t row, int32_t j, float* f) {
+    if (d.t == 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = 1.0f;
+        return;
+    }
+    const Philox u = philox(d, step, (uint32_t)row, (uint32_t)j >> 3);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const uint32_t n = N == 4 && (j & 4) ? u.at(e + 4) : u.at(e);
+        f[e] = n >= d.t ? d.factor : 0.0f;
+    }
+}
+// A dropped element is 0 whatever it was.
+__device__ __forceinline__ float dropped(float v, float f) { return f > 0.0f ? v * f : 0.0f; }
+
+// A wave's part of a gated product: a lane holds gate and up of the same columns, in fragments NP apart.
+template <int NQ, int NP, int OB>
+__device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ][2 * NP], const int32_t (&out_row)[2],
+                                           int32_t j0, uint64_t step) {
+    constexpr int FQ = 2 * NQ, Y = OB == 2 ? 2 : 1, N = 4 * Y;
+    const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
+    const int32_t jw = j0 + (wave & 1) * 16 * NP + g * N;
+#pragma unroll
+    for (int x = 0; x < FQ; ++x) {
+        const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+#pragma unroll
+        for (int y = 0; y < NP; y += Y) {
+            const int32_t j = jw + y * 16, left = (int32_t)a.J - j;
+            float u[N], v[N], f[N], h[N];
+#pragma unroll
+            for (int s = 0; s < Y; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (NQ * NP > 4) {
+                        u[s * 4 + e] = acc_read(acc[x][y + s][e]);
+                        v[s * 4 + e] = acc_read(acc[x][y + NP + s][e]);
+                    } else {
+                        u[s * 4 + e] = acc[x][y + s][e];
+                        v[s * 4 + e] = acc[x][y + NP + s][e];
+                    }
+                }
+            dropout_factors<N>(a.drop, step, row, j, f);
+            if (a.act == AH_SILU) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) h[e] = dropped(activate(AH_SILU, u[e]) * v[e], f[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) h[e] = dropped(activate(a.act, u[e]) * v[e], f[e]);
+            }
+            if (row >= 0 && left > 0) {
+                if constexpr (OB == 2) {
+                    put_bf16<N>(static_cast<char*>(a.out) + (row * a.J + j) * 2, h, left);
+                } else {
+                    char* const o = static_cast<char*>(a.out) + (row * a.J + j) * 4;
+                    const v4i w = {__builtin_bit_cast(int, h[0]), __builtin_bit_cast(int, h[1]),
+                                   __builtin_bit_cast(int, h[2]), __builtin_bit_cast(int, h[3])};
+                    if (left >= 4)
+                        __builtin_memcpy(o, &w, 16);
+                    else
+                        store_left<4>(o, w, left);
+                }
+                if (a.pre) {
+                    char* const o = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
+                    put_bf16<N>(o, u, left);
+                    put_bf16<N>(o + a.J * 2, v, left);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+// A wave's part of the gradient: dh becomes (da, db) and h.
+template <int NQ, int NP>
+__device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ][2 * NP], const int32_t (&out_row)[2],
+                                           int32_t leaf, int32_t j0, uint64_t step) {
+    static_assert(NQ * NP <= 4, "");
+    constexpr int FQ = 2 * NQ, FP = 2 * NP, N = 4;
+    const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
+    const int32_t jw = j0 + (wave & 1) * 32 * NP + g * N;
+#pragma unroll
+    for (int x = 0; x < FQ; ++x) {
+        const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+        float u[FP][N], v[FP][N];
+#pragma unroll
+        for (int y = 0; y < FP; ++y) {
+            const int32_t j = jw + y * 16, left = row < 0 ? 0 : (int32_t)a.J - j;
+            const char* const p = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
+            get_bf16<N>(p, u[y], left);
+            get_bf16<N>(p + a.J * 2, v[y], left);
+        }
+#pragma unroll
+        for (int y = 0; y < FP; ++y) {
+            const int32_t j = jw + y * 16, left = row < 0 ? 0 : (int32_t)a.J - j;
+            float f[N], da[N], db[N], h[N];
+            dropout_factors<N>(a.drop, step, row, j, f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float t, dt;
+                activate_grad(a.act, u[y][e], &t, &dt);
+                const float dh = acc[x][y][e], k = leaf < 0 ? 0.0f : f[e];
+                da[e] = dropped(dh * v[y][e] * dt, k);
+                db[e] = dropped(dh * t, k);
+                h[e] = dropped(t * v[y][e], k);
+            }
+            if (left > 0) {
+                char* const o = static_cast<char*>(a.out) + ((int64_t)row * 2 * a.J + j) * 2;
+                put_bf16<N>(o, da, left);
+                put_bf16<N>(o + a.J * 2, db, left);
+                if (a.hidden) put_bf16<N>(a.hidden + (row * a.J + j) * 2, h, left);
+            }
+        }
+    }
+}
+
 struct Tile {
     int32_t leaf;       // -1: rows of no leaf (their outputs are zero)
     int32_t p0, p1;     // grouped rows: of the tile (forward, dx; int8: plain rows), of the leaf (dw)
@@ -336,12 +515,13 @@ __device__ __forceinline__ Tile uniform(Tile t) {
     return t;
 }
 
+constexpr int kScaleBuf = 512;
 struct LocateShared {
     int32_t wave_sum[kNT / 64];
     Tile next[2];
 };
 __device__ __forceinline__ int32_t leaf_start(const ProdArgs& a, int32_t l) {  // inside [0, T] whatever the array holds
-    const int64_t o = a.off[l];
+    const int64_t o = a.off ? a.off[l] : l ? a.T : 0;
     return (int32_t)(o < 0 ? 0 : o > a.T ? a.T : o);
 }
 // Rows of entry e: a leaf, or (L, L + 1) the rows after the last and before the first leaf.
@@ -391,15 +571,16 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // and 442 us instead of 446, on zeros 337.
 template <int MODE, int NQ, int NP, int OB, bool DMA>
 __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(ProdArgs a) {
-    constexpr int ELEM = MODE == kI8 ? 1 : 2, FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
-    constexpr bool QCOL = MODE == kDw, PCOL = MODE >= kDx, RAGGED = MODE == kFwd || MODE == kDx;
-    constexpr bool PERM = kPerm<MODE, OB>;
-    constexpr int TQ = NQ * 64, TP = NP * 64, STEP = 128 / ELEM;
+    constexpr int ELEM = elem_bytes(MODE), FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
+    constexpr bool QCOL = MODE == kDw, PCOL = p_by_col(MODE), RAGGED = is_ragged(MODE), PLAIN = is_plain(MODE);
+    constexpr bool PERM = kPerm<MODE, OB>, GATE = MODE == kGate, F8 = is_f8(MODE);
+    constexpr int TQ = NQ * 64, TP = NP * 64 / (GATE ? 2 : 1), STEP = 128 / ELEM;
     constexpr int BUF = NB * kBlock;
-    constexpr int QR = QCOL ? 2 : MODE == kI8 ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : 2 * NQ;
+    constexpr int QR = QCOL ? 2 : PLAIN ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : 2 * NQ;
     __shared__ __align__(1024) char lds[(DMA ? 2 : 1) * BUF];
-    __shared__ __align__(16) char turns[OB == 4 ? 4 * 16 * kTurnPitch<NP> : 16];
-    __shared__ __align__(16) float scales[MODE == kI8 ? 128 * NP + 64 * NQ : 4];
+    __shared__ __align__(16) char turns[OB == 4 && !GATE ? 4 * 16 * kTurnPitch<NP> : 16];
+    __shared__ __align__(16) float scales[MODE == kI8 ? 128 * NP + 64 * NQ : F8 ? 64 * NP : 4];
+    __shared__ __align__(16) char sbytes[F8 ? 2 * kScaleBuf : 16];  // float8: a step's scale bytes, Q's 256 and P's
     __shared__ LocateShared sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wq = wave >> 1, wp = wave & 1, g = lane >> 4, li = lane & 15;
@@ -495,9 +676,9 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     Tile w;                               // the tile that is loaded
     const char* qrow[QR];                 // row operand: its rows; by column: this step's memory rows
-    const char* prow[MODE == kDw ? 2 : 1];
-    uint32_t poff[PCOL ? 1 : 2 * NP];     // rows that follow one another: offsets from prow[0], qrow[0]
-    uint32_t qoff[MODE == kI8 ? 2 * NQ : 1];
+    const char* prow[MODE == kDw || GATE ? 2 : 1];
+    uint32_t poff[PCOL ? 1 : GATE ? NP : 2 * NP];  // rows that follow one another: offsets from prow[0], qrow[0]
+    uint32_t qoff[PLAIN ? 2 * NQ : 1];
     int32_t slot[SLOTS];                  // slots of a tile's rows; dw: of the next step's memory rows
 
     // What the order holds is kept as it was read until it is used, a step later: a check beside the
@@ -557,7 +738,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             const int32_t i = wq * 32 * NQ + u * 64 + lane;
             if constexpr (MODE == kDw)
                 rows[u] = n.i0 + i < a.I ? n.i0 + i : -1;
-            else if constexpr (MODE == kI8)
+            else if constexpr (PLAIN)
                 rows[u] = n.p0 + i < n.p1 ? n.p0 + i : -1;
             else
                 rows[u] = n.p0 + i < n.p1 && known(rows[u]) ? rows[u] : -1;
@@ -565,7 +746,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     };
     auto set_addresses = [&]() {
         const int rr = here(tid) >> 3;
-        if constexpr (MODE == kI8) {
+        if constexpr (PLAIN) {
             qrow[0] = a.q + w.p0 * a.qs + rc;
 #pragma unroll
             for (int s = 0; s < 2 * NQ; ++s) {
@@ -576,19 +757,28 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 #pragma unroll
             for (int s = 0; s < 2 * NQ; ++s) {
                 int32_t r = known(slot[s]) ? slot[s] : 0;
-                if constexpr (MODE == kFwd) r = (int32_t)query_of(a, (uint32_t)r);
+                if constexpr (MODE == kFwd || GATE) r = (int32_t)query_of(a, (uint32_t)r);
                 qrow[s] = a.q + (int64_t)r * a.qs + rc;
             }
         }
         const char* pbase = a.p + (RAGGED && w.leaf > 0 ? w.leaf * a.pg : 0);
-        if constexpr (!PCOL) {
+        if constexpr (GATE) {
+            // Rows of the tile: for each of the wave's columns' halves, 16 NP gate rows, then their up rows.
+            prow[0] = pbase + w.j0 * a.ps + rc;
+            prow[1] = prow[0] + a.J * a.ps;
+#pragma unroll
+            for (int s = 0; s < NP; ++s) {
+                const int r = s * 32 + rr;
+                poff[s] = w.j0 + r < a.J ? (uint32_t)(r * a.ps) : 0u;
+            }
+        } else if constexpr (!PCOL) {
             prow[0] = pbase + w.j0 * a.ps + rc;
 #pragma unroll
             for (int s = 0; s < 2 * NP; ++s) {
                 const int r = s * 32 + rr;
                 poff[s] = w.j0 + r < a.J ? (uint32_t)(r * a.ps) : 0u;
             }
-        } else if constexpr (MODE == kDx) {
+        } else if constexpr (MODE != kDw) {
             prow[0] = pbase + rr * a.ps + (int64_t)w.j0 * 2 + cc;
         }
     };
@@ -600,10 +790,14 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         if (c < 2 * NP) {
             const int h = c >> 1;
             if constexpr (PCOL) *before = (int64_t)w.j0 * 2 + h * 128 + cc;
-            if constexpr (!PCOL) {
+            if constexpr (GATE) {
+                constexpr int H = NP / 2;  // groups of 32 rows of a half
+                *valid = w.red * ELEM - (u * 128 + rc);
+                return prow[c / H & 1] + poff[c / (2 * H) * H + c % H] + u * 128;
+            } else if constexpr (!PCOL) {
                 *valid = w.red * ELEM - (u * 128 + rc);
                 return prow[0] + poff[c] + u * 128;
-            } else if constexpr (MODE == kDx) {
+            } else if constexpr (MODE != kDw) {
                 const int r = u * STEP + s * 32;
                 *valid = r + rr < w.red ? ((int32_t)a.J - w.j0) * 2 - (h * 128 + cc) : 0;
                 return prow[0] + r * a.ps + h * 128;
@@ -616,7 +810,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             if constexpr (QCOL) *before = (int64_t)w.i0 * 2 + h * 128 + cc;
             if constexpr (!QCOL) {
                 *valid = w.red * ELEM - (u * 128 + rc);
-                if constexpr (MODE == kI8)
+                if constexpr (PLAIN)
                     return qrow[0] + qoff[c - 2 * NP] + u * 128;
                 else
                     return qrow[c - 2 * NP] + u * 128;
@@ -675,7 +869,36 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     typedef typename Acc<MODE>::type acc_t;
     acc_t acc[FQ][FP];
+    // Two sets of fragments; float8 keeps whole steps: pf[h] is the 64-byte half h of every column fragment, qf[h] both
+    // halves of the row fragments of half-step h.
     v4i pf[2][FP], qf[2][FQ];
+    int psc[F8 ? FP : 1], qsc[F8 ? FQ : 1];  // their scale bytes
+    const uint32_t sbase = lds_addr(sbytes);
+    auto byte_at = [&](uint32_t at) -> int {
+        return *(const __attribute__((address_space(3))) uint8_t*)(lds_char)(uintptr_t)at;
+    };
+    auto read_p8 = [&](int y, int b) {
+        pf[0][y] = read_p(y, 0, b * BUF);
+        pf[1][y] = read_p(y, 1, b * BUF);
+        if constexpr (F8)
+            psc[y] = byte_at(sbase + b * kScaleBuf + 256 + wp * 32 * NP + pl + (PERM ? (y >> 1) * 32 + (y & 1) * 4 : y * 16));
+    };
+    auto read_q8 = [&](int h, int x, int b) {  // x of the half's FQ / 2
+        const int n = h * FQ / 2 + x;
+        qf[h][2 * x] = read_q(n, 0, b * BUF);
+        qf[h][2 * x + 1] = read_q(n, 1, b * BUF);
+        if constexpr (F8) qsc[n] = byte_at(sbase + b * kScaleBuf + wq * 32 * NQ + n * 16 + li);
+    };
+    // A step's scale bytes: wave 0 brings the rows', wave 1 the columns'.  Rows past the last of the pitch repeat its first.
+    auto load_scale_bytes = [&](int u, uint32_t b) {
+        if constexpr (F8) {
+            if (wave < 2) {
+                const int32_t steps_of = (int32_t)(a.red / STEP), us = u < steps_of ? u : steps_of - 1;
+                const int64_t pitch = wave ? a.ppitch : a.qpitch, r = (wave ? w.j0 : w.p0) + 4 * (int64_t)lane;
+                dma4((wave ? a.psc : a.qsc) + us * pitch + (r < pitch ? r : 0), sbase + b * kScaleBuf + wave * 256);
+            }
+        }
+    };
     auto load = [&](int u, int c, uint32_t buf) {
         int32_t valid;
         int64_t before;
@@ -684,6 +907,29 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     };
     // One half-step: the matrix instructions of fragment set kk; between them the reads of
     // the other set from `buf` and (kk = 1) the loads of step u into the other buffer.
+    // float8: half-step kk multiplies half of the row fragments with all column fragments; the first reads the other half,
+    // the second, once a column fragment is done with, the next step's, and the first row fragments.
+    auto half_step8 = [&](int kk, uint32_t buf, int u) {
+        const int b = buf ? 1 : 0;
+#pragma unroll
+        for (int y = 0; y < FP; ++y) {
+#pragma unroll
+            for (int x = 0; x < FQ / 2; ++x) {
+                const int n = kk * FQ / 2 + x;
+                if constexpr (F8)
+                    acc[n][y] = mma8<MODE>(pf[0][y], pf[1][y], qf[kk][2 * x], qf[kk][2 * x + 1], acc[n][y], psc[y], qsc[n]);
+            }
+            if (kk == 1) {
+                read_p8(y, b);
+#pragma unroll
+                for (int c = y * 2 * NB / FP; c < (y + 1) * 2 * NB / FP; ++c) load(u, c, BUF - buf);
+                if (y == FP - 1) load_scale_bytes(u, 1 - b);
+            }
+#pragma unroll
+            for (int x = y * (FQ / 2) / FP; x < (y + 1) * (FQ / 2) / FP; ++x) read_q8(kk ^ 1, x, b);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
     auto half_step = [&](int kk, uint32_t buf, int u) {
         constexpr int N = FQ + FP;  // groups: fragments to read, chunks to load
 #pragma unroll
@@ -710,12 +956,18 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     auto load_scales = [&](const Tile& n, float(&v)[3]) {
         const int tid = here(threadIdx.x);
         const int32_t j = n.j0 + tid < a.J ? n.j0 + tid : (int32_t)a.J - 1, r = n.p0 + tid < n.p1 ? n.p0 + tid : n.p0;
-        v[0] = a.sw[j];
         v[1] = a.bias ? a.bias[j] : 0.0f;
-        v[2] = a.sx[r];
+        if constexpr (MODE == kI8) {
+            v[0] = a.sw[j];
+            v[2] = a.sx[r];
+        }
     };
     auto keep_scales = [&](const float(&v)[3]) {
         const int tid = here(threadIdx.x);
+        if constexpr (F8) {
+            if (tid < 64 * NP) scales[tid] = v[1];
+            return;
+        }
         if (tid < 64 * NP) {
             scales[tid] = v[0];
             scales[64 * NP + tid] = v[1];
@@ -723,8 +975,15 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         if (tid < 64 * NQ) scales[128 * NP + tid] = v[2];
     };
 
-    char* const turn = turns + (OB == 4 ? wave * 16 * kTurnPitch<NP> : 0);
-
+    const uint64_t call_step = is_gated(MODE) && a.drop.t ? step_of_call(a.drop) : 0;
+    auto store = [&](const int32_t(&rows)[2], const Tile& n) {
+        if constexpr (GATE)
+            store_gate<NQ, NP, OB>(a, acc, rows, n.j0, call_step);
+        else if constexpr (MODE == kGrad)
+            store_grad<NQ, NP>(a, acc, rows, n.leaf, n.j0, call_step);
+        else
+            store_part<MODE, NQ, NP, OB>(a, acc, scales, turns + (OB == 4 ? wave * 16 * kTurnPitch<NP> : 0), rows, n.leaf, n.j0);
+    };
     int64_t t = tbeg + (blockIdx.x >> 3);
     const int64_t hop = gridDim.x >> 3;
     if (t >= tend) return;
@@ -768,6 +1027,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
 #pragma unroll
             for (int c = 0; c < 2 * NB; ++c) load(ul, c, ul * BUF);
+            load_scale_bytes(ul, ul);
         }
         us = 1;
         advance_order();
@@ -776,19 +1036,29 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 #pragma unroll
         for (int u = 0; u < 2; ++u) rows_c[u] = rows_l[u];
         clear();
-        land<2 * NB>();
+        land<2 * NB>();  // (float8: a wave has up to one more of step 1 in flight)
+        if constexpr (F8) {
 #pragma unroll
-        for (int x = 0; x < FQ; ++x) qf[0][x] = read_q(x, 0, 0);
+            for (int x = 0; x < FQ / 2; ++x) read_q8(0, x, 0);
 #pragma unroll
-        for (int x = 0; x < FP; ++x) pf[0][x] = read_p(x, 0, 0);
+            for (int y = 0; y < FP; ++y) read_p8(y, 0);
+        } else {
+#pragma unroll
+            for (int x = 0; x < FQ; ++x) qf[0][x] = read_q(x, 0, 0);
+#pragma unroll
+            for (int x = 0; x < FP; ++x) pf[0][x] = read_p(x, 0, 0);
+        }
         for (uint32_t cur = 0;; cur = BUF - cur) {
             float sv[3] = {};
-            if constexpr (MODE == kI8) {
+            if constexpr (PLAIN) {
                 if (uc == 0) load_scales(wc, sv);
             }
-            half_step(0, cur, 0);
+            if constexpr (F8)
+                half_step8(0, cur, 0);
+            else
+                half_step(0, cur, 0);
             land<0>();
-            if constexpr (MODE == kI8) {
+            if constexpr (PLAIN) {
                 if (uc == 0) keep_scales(sv);
             }
             if (ul == w.nt) {
@@ -800,11 +1070,14 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
             if constexpr (MODE == kDw) set_rows(ul, slot);
             advance_order();
-            half_step(1, BUF - cur, ul++);
+            if constexpr (F8)
+                half_step8(1, BUF - cur, ul++);
+            else
+                half_step(1, BUF - cur, ul++);
             if (++uc < wc.nt) continue;
             if constexpr (NQ * NP > 4) settle();
             out_rows(wc, rows_c);
-            store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows_c, wc.leaf, wc.j0);
+            store(rows_c, wc);
             t += hop;
             if (t >= tend) break;
             wc = w;
@@ -859,7 +1132,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                 }
             }
             out_rows(w, rows);
-            store_part<MODE, NQ, NP, OB>(a, acc, scales, turn, rows, w.leaf, w.j0);
+            store(rows, w);
             t += hop;
             if (t >= tend) break;
             __syncthreads();
@@ -931,10 +1204,10 @@ __device__ __forceinline__ float step_of(float m) { return m < INFINITY ? m / 12
 constexpr int kRowWaves = 8;
 template <int MODE, int FR, bool WHOLE, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
-    constexpr int ELEM = MODE == kI8 ? 1 : 2, U = 4;
+    constexpr int ELEM = elem_bytes(MODE), U = 4, G = MODE == kGate ? 2 : 1;
     static_assert(XB == 0 || (MODE == kI8 && FR == 1 && WHOLE), "");
     typedef typename Acc<MODE>::type acc_t;
-    __shared__ acc_t part[kRowWaves][FR][64];
+    __shared__ acc_t part[kRowWaves][G * FR][64];
     __shared__ float most[kRowWaves][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, li = lane & 15;
@@ -942,6 +1215,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
     const int32_t s0 = steps * wave / kRowWaves, s1 = steps * (wave + 1) / kRowWaves;
     const int32_t j = blockIdx.x * 16 + g * 4;  // this lane's four output columns
     const int32_t leaf = MODE == kI8 ? 0 : blockIdx.y;
+    const uint64_t call_step = MODE == kGate && a.drop.t ? step_of_call(a.drop) : 0;
     auto put = [&](int32_t row, v4f v) {
         if (a.out_f32) {
             float* o = static_cast<float*>(a.out) + row * a.J + j;
@@ -974,6 +1248,12 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
             const int32_t left = (int32_t)a.J - c, ob = a.out_f32 ? 4 : 2;
             char* o = static_cast<char*>(a.out) + (row * a.J + c) * ob;
             for (int32_t e = 0; e < (left < 4 ? left : 4) * ob; e += 2) *reinterpret_cast<uint16_t*>(o + e) = 0;
+            if (MODE == kGate && a.pre) {
+                const float none[4] = {};
+                char* const p = a.pre + ((int64_t)row * 2 * a.J + c) * 2;
+                put_bf16<4>(p, none, left);
+                put_bf16<4>(p + a.J * 2, none, left);
+            }
         }
         return;
     }
@@ -1021,7 +1301,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
             }
             qrow[f] = a.q + (int64_t)r * a.qs;
         }
-        v4i pv[U], qv[U][FR], xv[XB > 0 ? U : 1][XB > 0 ? XB : 1];
+        v4i pv[U], uv[G == 2 ? U : 1], qv[U][FR], xv[XB > 0 ? U : 1][XB > 0 ? XB : 1];
         auto load = [&](int32_t s) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -1036,6 +1316,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                             xv[u][c] = o < kb ? *reinterpret_cast<const v4i*>(qrow[0] + (o * XB + c * 16)) : v4i{0, 0, 0, 0};
                     }
                     pv[u] = fetch(prow, o);
+                    if constexpr (G == 2) uv[u] = fetch(prow + a.J * a.ps, o);
                 }
         };
         load(s0);
@@ -1069,9 +1350,9 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
             for (int w = 1; w < kRowWaves; ++w) m = fmaxf(m, most[w][li]);
             sx = step_of(m);
         }
-        acc_t acc[FR];
+        acc_t acc[G * FR];
 #pragma unroll
-        for (int f = 0; f < FR; ++f) acc[f] = acc_t{0, 0, 0, 0};
+        for (int f = 0; f < G * FR; ++f) acc[f] = acc_t{0, 0, 0, 0};
         for (int32_t s = s0; s < s1; s += U) {
             if (s > s0) load(s);
             if constexpr (XB > 0) {
@@ -1093,11 +1374,14 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
             for (int u = 0; u < U; ++u)
                 if (s + u < s1) {
 #pragma unroll
-                    for (int f = 0; f < FR; ++f) acc[f] = mma<MODE>(pv[u], qv[u][f], acc[f]);
+                    for (int f = 0; f < FR; ++f) {
+                        acc[f] = mma<MODE>(pv[u], qv[u][f], acc[f]);
+                        if constexpr (G == 2) acc[FR + f] = mma<MODE>(uv[u], qv[u][f], acc[FR + f]);
+                    }
                 }
         }
 #pragma unroll
-        for (int f = 0; f < FR; ++f) part[wave][f][lane] = acc[f];
+        for (int f = 0; f < G * FR; ++f) part[wave][f][lane] = acc[f];
         __syncthreads();
 #pragma unroll
         for (int f = 0; f < FR; ++f)
@@ -1111,6 +1395,20 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                     for (int e = 0; e < 4; ++e) {
                         v[e] = (float)t[e] * sx * sw[e];
                         if (a.bias) v[e] += bias[e];
+                    }
+                } else if constexpr (G == 2) {
+                    v4f up = part[0][FR + f][lane];
+#pragma unroll
+                    for (int w = 1; w < kRowWaves; ++w) up += part[w][FR + f][lane];
+                    float drop[4];
+                    dropout_factors<4>(a.drop, call_step, out_row[f], j, drop);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = dropped(activate(a.act, t[e]) * up[e], drop[e]);
+                    if (a.pre) {
+                        const float gates[4] = {t[0], t[1], t[2], t[3]}, ups[4] = {up[0], up[1], up[2], up[3]};
+                        char* const p = a.pre + ((int64_t)out_row[f] * 2 * a.J + j) * 2;
+                        put_bf16<4>(p, gates, (int32_t)a.J - j);
+                        put_bf16<4>(p + a.J * 2, ups, (int32_t)a.J - j);
                     }
                 } else {
                     v = t;
@@ -1130,7 +1428,7 @@ inline bool chunked(const void* p, int64_t stride_bytes, int64_t width_bytes) {
 template <int MODE>
 int64_t row_tiles(const ProdArgs& a, int64_t TQ, bool most) {
     if (MODE == kDw) return (a.I + TQ - 1) / TQ * a.L;
-    if (MODE == kI8) return (a.T + TQ - 1) / TQ;
+    if (is_plain(MODE)) return (a.T + TQ - 1) / TQ;
     return a.T / TQ + (most ? a.L + 2 : (a.T < a.L ? a.T : a.L) / 2 + 1);
 }
 
@@ -1143,7 +1441,8 @@ int64_t row_tiles(const ProdArgs& a, int64_t TQ, bool most) {
 template <int MODE>
 int tile_shape(const ProdArgs& a) {
     auto time = [&](int64_t TQ, int64_t TP, int64_t resident, double round) {
-        return (double)((row_tiles<MODE>(a, TQ, false) * ((a.J + TP - 1) / TP) + resident - 1) / resident) * round;
+        const int64_t J = MODE == kGate ? 2 * a.J : a.J;
+        return (double)((row_tiles<MODE>(a, TQ, false) * ((J + TP - 1) / TP) + resident - 1) / resident) * round;
     };
     const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / 0.97),
                  t2 = time(128, 128, 2 * kCUs, 8 / 0.85);
@@ -1152,7 +1451,7 @@ int tile_shape(const ProdArgs& a) {
 
 template <int MODE, int NQ, int NP, bool DMA>
 hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
-    constexpr int TQ = NQ * 64, TP = NP * 64;
+    constexpr int TQ = NQ * 64, TP = NP * 64 / (MODE == kGate ? 2 : 1);
     const int64_t np = (a.J + TP - 1) / TP, each = row_tiles<MODE>(a, TQ, true) * np;
     const int64_t resident = kCUs * (NQ * NP > 4 ? 1 : 2);
     int64_t wgs = (each + 7) / 8 * 8;
@@ -1162,10 +1461,13 @@ hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
     }
     if ((MODE != kDw || wgs * kNT > kMaxGridItems) && wgs > resident) wgs = resident;
     const dim3 grid((uint32_t)wgs);
-    if (a.out_f32)
-        hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 4, DMA>), grid, dim3(kNT), 0, stream, a);
-    else
-        hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 2, DMA>), grid, dim3(kNT), 0, stream, a);
+    if constexpr (MODE != kGrad) {
+        if (a.out_f32) {
+            hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 4, DMA>), grid, dim3(kNT), 0, stream, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 2, DMA>), grid, dim3(kNT), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -1200,11 +1502,11 @@ hipError_t launch_rows(const ProdArgs& a, bool whole, hipStream_t stream) {
 
 template <int MODE>
 hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
-    const int e = MODE == kI8 ? 1 : 2;
+    const int e = elem_bytes(MODE);
     bool whole;
     if (MODE == kDw)
         whole = chunked(a.q, a.qs, a.I * e) && chunked(a.p, a.ps, a.J * e);
-    else if (MODE == kDx)
+    else if (MODE == kDx || MODE == kGrad)
         whole = chunked(a.q, a.qs, a.red * e) && chunked(a.p, a.ps, a.J * e);
     else
         whole = chunked(a.q, a.qs, a.red * e) && chunked(a.p, a.ps, 0);
@@ -1214,16 +1516,18 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     a.fan_shift = 31 + l;
     a.fan_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + fan - 1) / fan);
     const int64_t pitch = a.J * (a.out_f32 ? 4 : 2);
-    a.bypass = MODE != kFwd && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
-    if constexpr (MODE == kI8 || MODE == kFwd) {
+    a.bypass = MODE != kFwd && MODE != kGate && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
+    if constexpr (MODE == kI8 || MODE == kFwd || MODE == kGate) {
         switch (row_fragments<MODE>(a)) {
             case 1: return launch_rows<MODE, 1>(a, whole, stream);
             case 2: return launch_rows<MODE, 2>(a, whole, stream);
             case 4: return launch_rows<MODE, 4>(a, whole, stream);
         }
     }
-    if (!whole) return launch_tiles<MODE, 2, 2, false>(a, stream);
-    if constexpr (MODE == kDw) {
+    if constexpr (!is_f8(MODE)) {
+        if (!whole) return launch_tiles<MODE, 2, 2, false>(a, stream);
+    }
+    if constexpr (MODE == kDw || MODE == kGrad) {
         return launch_tiles<MODE, 2, 2, true>(a, stream);
     } else {
         switch (tile_shape<MODE>(a)) {
