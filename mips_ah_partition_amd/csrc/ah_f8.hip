@@ -256,7 +256,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int6
                     for (int i = 0; i < 8; ++i) qv[u][0][i >> 2][i & 3] = codes4<XT>(v + i * 4, b);
                 }
 #pragma unroll
-                for (int f = 0; f < FR; ++f) acc[f] = mma8<MODE>(pv[u][0], pv[u][1], qv[u][f][0], qv[u][f][1], acc[f], sp[u], sq[u][f]);
+                for (int f = 0; f < FR; ++f) acc[f] = mma8<MODE>(halves(pv[u][0], pv[u][1]), halves(qv[u][f][0], qv[u][f][1]), acc[f], sp[u], sq[u][f]);
             }
     }
 #pragma unroll

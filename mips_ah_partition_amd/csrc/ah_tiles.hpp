@@ -131,11 +131,12 @@ __device__ __forceinline__ typename Acc<MODE>::type mma(v4i p, v4i q, typename A
                                                        0, 0);
 }
 
-// 128 bytes of the sum: halves lo and hi of 64; scale bytes in the low bytes of sp and sq.
+// 128 bytes of the sum; scale bytes in the low bytes of sp and sq.
+__device__ __forceinline__ v8i halves(v4i lo, v4i hi) {
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 template <int MODE>
-__device__ __forceinline__ v4f mma8(v4i plo, v4i phi, v4i qlo, v4i qhi, v4f c, int sp, int sq) {
-    const v8i p = __builtin_shufflevector(plo, phi, 0, 1, 2, 3, 4, 5, 6, 7),
-              q = __builtin_shufflevector(qlo, qhi, 0, 1, 2, 3, 4, 5, 6, 7);
+__device__ __forceinline__ v4f mma8(v8i p, v8i q, v4f c, int sp, int sq) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, (MODE - kF8) >> 1 & 1, (MODE - kF8) & 1, 0, sp, 0,
                                                             sq);
 }
@@ -359,18 +360,23 @@ __device__ __forceinline__ void put_bf16(char* o, const float* v, int32_t left) 
     else if (left > 0)
         store_left<2>(o, v4i{(int)w[0], (int)w[1], (int)w[N / 2 - 2], (int)w[N / 2 - 1]}, left);
 }
-template <int N>
-__device__ __forceinline__ void get_bf16(const char* p, float* v, int32_t left) {
-    uint16_t b[N] = {};
-    if (left >= N) {
-        __builtin_memcpy(b, p, 2 * N);
+// Eight, as they lie in memory (zeros for those that do not exist).
+__device__ __forceinline__ v4i get_bf16x8(const char* p, int32_t left) {
+    v4i r = {0, 0, 0, 0};
+    if (left >= 8) {
+        __builtin_memcpy(&r, p, 16);
     } else {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (e < left) __builtin_memcpy(b + e, p + 2 * e, 2);
+        for (int e = 0; e < 8; ++e) {
+            uint16_t b = 0;
+            if (e < left) __builtin_memcpy(&b, p + 2 * e, 2);
+            r[e >> 1] |= (int)((uint32_t)b << (e & 1 ? 16 : 0));
+        }
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = __uint_as_float((uint32_t)b[e] << 16);
+    return r;
+}
+__device__ __forceinline__ float bf16_at(v4i r, int e) {
+    return __uint_as_float(e & 1 ? (uint32_t)r[e >> 1] & 0xFFFF0000u : (uint32_t)r[e >> 1] << 16);
 }
 // Factors of N (4 or 8) columns from j on (a multiple of N) of a row.
 template <int N>
@@ -447,38 +453,57 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
     }
 }
 
-// A wave's part of the gradient: dh becomes (da, db) and h.
+// Two column fragments, a lane holding columns 4 g .. 4 g + 3 of each, become eight consecutive columns: with quarters
+// of a wave g = 0 .. 3, those of fragment g & 1 from 8 (g >> 1) on.
+__device__ __forceinline__ void eight_columns(v4f f0, v4f f1, float* v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto t = __builtin_amdgcn_permlane16_swap(__float_as_uint(f0[e]), __float_as_uint(f1[e]), false, false);
+        v[e] = __uint_as_float(t[0]);
+        v[4 + e] = __uint_as_float(t[1]);
+    }
+}
+// A wave's part of the gradient: dh becomes (da, db) and h.  What the projections' loads take is hidden by asking for
+// the next fragment row's before this one's arithmetic.
 template <int NQ, int NP>
 __device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ][2 * NP], const int32_t (&out_row)[2],
                                            int32_t leaf, int32_t j0, uint64_t step) {
     static_assert(NQ * NP <= 4, "");
-    constexpr int FQ = 2 * NQ, FP = 2 * NP, N = 4;
+    constexpr int FQ = 2 * NQ, N = 8;
     const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
-    const int32_t jw = j0 + (wave & 1) * 32 * NP + g * N;
+    const int32_t jw = j0 + (wave & 1) * 32 * NP + (g & 1) * 16 + (g >> 1) * 8;
+    v4i u[2][NP], v[2][NP];
+    int32_t rows[2];
+    auto ask = [&](int x) {
+        const int32_t row = rows[x & 1] = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+#pragma unroll
+        for (int z = 0; z < NP; ++z) {
+            const int32_t j = jw + z * 32, left = row < 0 ? 0 : (int32_t)a.J - j;
+            const char* const p = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
+            u[x & 1][z] = get_bf16x8(p, left);
+            v[x & 1][z] = get_bf16x8(p + a.J * 2, left);
+        }
+    };
+    ask(0);
 #pragma unroll
     for (int x = 0; x < FQ; ++x) {
-        const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
-        float u[FP][N], v[FP][N];
+        if (x + 1 < FQ) ask(x + 1);
+        const int32_t row = rows[x & 1];
 #pragma unroll
-        for (int y = 0; y < FP; ++y) {
-            const int32_t j = jw + y * 16, left = row < 0 ? 0 : (int32_t)a.J - j;
-            const char* const p = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
-            get_bf16<N>(p, u[y], left);
-            get_bf16<N>(p + a.J * 2, v[y], left);
-        }
-#pragma unroll
-        for (int y = 0; y < FP; ++y) {
-            const int32_t j = jw + y * 16, left = row < 0 ? 0 : (int32_t)a.J - j;
-            float f[N], da[N], db[N], h[N];
+        for (int z = 0; z < NP; ++z) {
+            const int32_t j = jw + z * 32, left = row < 0 ? 0 : (int32_t)a.J - j;
+            float f[N], dh[N], da[N], db[N], h[N];
+            eight_columns(acc[x][2 * z], acc[x][2 * z + 1], dh);
             dropout_factors<N>(a.drop, step, row, j, f);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
+                const bool keep = f[e] > 0.0f && leaf >= 0;  // else all zero, whatever the projections hold
+                const float up = keep ? bf16_at(v[x & 1][z], e) * f[e] : 0.0f, d = keep ? dh[e] : 0.0f;
                 float t, dt;
-                activate_grad(a.act, u[y][e], &t, &dt);
-                const float dh = acc[x][y][e], k = leaf < 0 ? 0.0f : f[e];
-                da[e] = dropped(dh * v[y][e] * dt, k);
-                db[e] = dropped(dh * t, k);
-                h[e] = dropped(t * v[y][e], k);
+                activate_grad(a.act, keep ? bf16_at(u[x & 1][z], e) : 0.0f, &t, &dt);
+                da[e] = d * up * dt;
+                db[e] = d * t * f[e];
+                h[e] = t * up;
             }
             if (left > 0) {
                 char* const o = static_cast<char*>(a.out) + ((int64_t)row * 2 * a.J + j) * 2;
@@ -869,34 +894,36 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     typedef typename Acc<MODE>::type acc_t;
     acc_t acc[FQ][FP];
-    // Two sets of fragments; float8 keeps whole steps: pf[h] is the 64-byte half h of every column fragment, qf[h] both
-    // halves of the row fragments of half-step h.
-    v4i pf[2][FP], qf[2][FQ];
+    // Two sets of fragments; float8 keeps whole steps: every column fragment, and the row fragments of half-step h.
+    v4i pf[F8 ? 1 : 2][F8 ? 1 : FP], qf[F8 ? 1 : 2][F8 ? 1 : FQ];
+    v8i p8[F8 ? FP : 1], q8[2][F8 ? FQ / 2 : 1];
     int psc[F8 ? FP : 1], qsc[F8 ? FQ : 1];  // their scale bytes
     const uint32_t sbase = lds_addr(sbytes);
     auto byte_at = [&](uint32_t at) -> int {
         return *(const __attribute__((address_space(3))) uint8_t*)(lds_char)(uintptr_t)at;
     };
     auto read_p8 = [&](int y, int b) {
-        pf[0][y] = read_p(y, 0, b * BUF);
-        pf[1][y] = read_p(y, 1, b * BUF);
+        p8[y] = halves(read_p(y, 0, b * BUF), read_p(y, 1, b * BUF));
         if constexpr (F8)
             psc[y] = byte_at(sbase + b * kScaleBuf + 256 + wp * 32 * NP + pl + (PERM ? (y >> 1) * 32 + (y & 1) * 4 : y * 16));
     };
     auto read_q8 = [&](int h, int x, int b) {  // x of the half's FQ / 2
         const int n = h * FQ / 2 + x;
-        qf[h][2 * x] = read_q(n, 0, b * BUF);
-        qf[h][2 * x + 1] = read_q(n, 1, b * BUF);
+        q8[h][x] = halves(read_q(n, 0, b * BUF), read_q(n, 1, b * BUF));
         if constexpr (F8) qsc[n] = byte_at(sbase + b * kScaleBuf + wq * 32 * NQ + n * 16 + li);
     };
-    // A step's scale bytes: wave 0 brings the rows', wave 1 the columns'.  Rows past the last of the pitch repeat its first.
+    // A step's scale bytes: even waves bring the rows', odd ones the columns' (two waves the same bytes: a branch here would
+    // end the matrix instructions' basic block, and the compiler moves them all behind it).  Rows past the last of the
+    // pitch repeat its first.
+    const int odd = __builtin_amdgcn_readfirstlane(wave & 1);
+    const char* const scale_bytes = odd ? a.psc : a.qsc;
+    const int64_t scale_pitch = odd ? a.ppitch : a.qpitch;
     auto load_scale_bytes = [&](int u, uint32_t b) {
         if constexpr (F8) {
-            if (wave < 2) {
-                const int32_t steps_of = (int32_t)(a.red / STEP), us = u < steps_of ? u : steps_of - 1;
-                const int64_t pitch = wave ? a.ppitch : a.qpitch, r = (wave ? w.j0 : w.p0) + 4 * (int64_t)lane;
-                dma4((wave ? a.psc : a.qsc) + us * pitch + (r < pitch ? r : 0), sbase + b * kScaleBuf + wave * 256);
-            }
+            const int32_t last = (int32_t)(a.red / STEP) - 1;
+            const int64_t r = (odd ? w.j0 : w.p0) + 4 * (int64_t)lane;
+            dma4(scale_bytes + (u < last ? u : last) * scale_pitch + (r < scale_pitch ? r : 0),
+                 sbase + b * kScaleBuf + odd * 256);
         }
     };
     auto load = [&](int u, int c, uint32_t buf) {
@@ -917,7 +944,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             for (int x = 0; x < FQ / 2; ++x) {
                 const int n = kk * FQ / 2 + x;
                 if constexpr (F8)
-                    acc[n][y] = mma8<MODE>(pf[0][y], pf[1][y], qf[kk][2 * x], qf[kk][2 * x + 1], acc[n][y], psc[y], qsc[n]);
+                    acc[n][y] = mma8<MODE>(p8[y], q8[kk][x], acc[n][y], psc[y], qsc[n]);
             }
             if (kk == 1) {
                 read_p8(y, b);
