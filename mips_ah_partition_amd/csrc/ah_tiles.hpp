@@ -54,6 +54,8 @@ constexpr int kBlock = 8192; // bytes of a block
 
 // Source of chunks that lie outside an operand (past its sum or its columns).
 __device__ const v4i zero_chunk = {0, 0, 0, 0};
+// Source of a whole step past the sum, for float8 operands whose rows are one step long: 256 rows of 128 bytes.
+__device__ const v4i zero_rows[2048] = {};
 
 struct ProdArgs {
     const char* q;         // row side
@@ -94,6 +96,10 @@ __device__ __forceinline__ void dma16(const char* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
                      __builtin_amdgcn_readfirstlane(lds)),
                  "v"(src));
+}
+// The same from a uniform address and an offset a lane, to a uniform one.
+__device__ __forceinline__ void dma16(const char* src, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
 }
 // 4 bytes a lane, at lds + 4 * lane.
 __device__ __forceinline__ void dma4(const char* src, uint32_t lds) {
@@ -772,11 +778,11 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     auto set_addresses = [&]() {
         const int rr = here(tid) >> 3;
         if constexpr (PLAIN) {
-            qrow[0] = a.q + w.p0 * a.qs + rc;
+            qrow[0] = a.q + w.p0 * a.qs + (F8 ? 0 : rc);
 #pragma unroll
             for (int s = 0; s < 2 * NQ; ++s) {
                 const int r = s * 32 + rr;
-                qoff[s] = w.p0 + r < w.p1 ? (uint32_t)(r * a.qs) : 0u;
+                qoff[s] = (w.p0 + r < w.p1 ? (uint32_t)(r * a.qs) : 0u) + (F8 ? rc : 0);
             }
         } else if constexpr (!QCOL) {
 #pragma unroll
@@ -797,11 +803,12 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                 poff[s] = w.j0 + r < a.J ? (uint32_t)(r * a.ps) : 0u;
             }
         } else if constexpr (!PCOL) {
-            prow[0] = pbase + w.j0 * a.ps + rc;
+            prow[0] = pbase + w.j0 * a.ps + (F8 ? 0 : rc);
 #pragma unroll
             for (int s = 0; s < 2 * NP; ++s) {
                 const int r = s * 32 + rr;
-                poff[s] = w.j0 + r < a.J ? (uint32_t)(r * a.ps) : 0u;
+                // (a step past the sum of float8 rows comes from zero_rows: rows of one step, or a tile of nothing)
+                poff[s] = (w.j0 + r < a.J && (!F8 || w.red > 0) ? (uint32_t)(r * a.ps) : 0u) + (F8 ? rc : 0);
             }
         } else if constexpr (MODE != kDw) {
             prow[0] = pbase + rr * a.ps + (int64_t)w.j0 * 2 + cc;
@@ -935,26 +942,51 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // One half-step: the matrix instructions of fragment set kk; between them the reads of
     // the other set from `buf` and (kk = 1) the loads of step u into the other buffer.
     // float8: half-step kk multiplies half of the row fragments with all column fragments; the first reads the other half,
-    // the second, once a column fragment is done with, the next step's, and the first row fragments.
+    // the second, once a column fragment is done with, the next step's, and the first row fragments.  Between two matrix
+    // instructions (32 clocks) stands one load or one fragment's reads: in a lump behind every fourth they cost the
+    // pipe (8192 x 4096 x 16384: 627 us with them).  So that a load is three instructions its address is a uniform one
+    // and a lane's offset, the same all along a tile.
+    const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(base + wave * 1024);
+    auto load8_chunk = [&](int u, int c, uint32_t buf) {
+        if constexpr (F8) {
+            const bool in = u * STEP < w.red;
+            const char* const src = in ? (c < 2 * NP ? prow[0] : qrow[0]) + u * STEP : reinterpret_cast<const char*>(zero_rows);
+            dma16(src, c < 2 * NP ? poff[c] : qoff[c - 2 * NP], lds_wave + buf + c * 4096);
+        }
+    };
     auto half_step8 = [&](int kk, uint32_t buf, int u) {
+        constexpr int H = FQ / 2;
         const int b = buf ? 1 : 0;
 #pragma unroll
         for (int y = 0; y < FP; ++y) {
 #pragma unroll
-            for (int x = 0; x < FQ / 2; ++x) {
-                const int n = kk * FQ / 2 + x;
-                if constexpr (F8)
-                    acc[n][y] = mma8<MODE>(p8[y], q8[kk][x], acc[n][y], psc[y], qsc[n]);
-            }
-            if (kk == 1) {
-                read_p8(y, b);
+            for (int x = 0; x < H; ++x) {
+                const int n = kk * H + x, at = y * H + x;
+                if constexpr (F8) acc[n][y] = mma8<MODE>(p8[y], q8[kk][x], acc[n][y], psc[y], qsc[n]);
+                if (kk == 1) {
+                    constexpr int S = FP * H;  // evenly: the four waves' 1 KB take the address unit 16 clocks each
 #pragma unroll
-                for (int c = y * 2 * NB / FP; c < (y + 1) * 2 * NB / FP; ++c) load(u, c, BUF - buf);
-                if (y == FP - 1) load_scale_bytes(u, 1 - b);
+                    for (int c = 0; c < 2 * NB; ++c)
+                        if (c * S / (2 * NB) == at) load8_chunk(u, c, BUF - buf);
+                    if (at == S - 2) load_scale_bytes(u, 1 - b);
+                    if (x == H - 1) read_p8(y, b);
+                }
+                if (x == 0 && y < H) read_q8(kk ^ 1, y, b);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        }
+        // The second half-step does not use the first's sums: without a use of them here the compiler moves the first's
+        // matrix instructions behind the barrier too, whose wait then nothing covers (554 us).
+        if (kk == 0) {
 #pragma unroll
-            for (int x = y * (FQ / 2) / FP; x < (y + 1) * (FQ / 2) / FP; ++x) read_q8(kk ^ 1, x, b);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int n = 0; n < H; ++n)
+#pragma unroll
+                for (int y = 0; y < FP; ++y) {
+                    if constexpr (NQ * NP > 4)
+                        held(acc[n][y]);
+                    else
+                        asm volatile("" : "+v"(acc[n][y]));
+                }
         }
     };
     auto half_step = [&](int kk, uint32_t buf, int u) {
@@ -1053,7 +1085,12 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                     set_rows(1, slot1);
             }
 #pragma unroll
-            for (int c = 0; c < 2 * NB; ++c) load(ul, c, ul * BUF);
+            for (int c = 0; c < 2 * NB; ++c) {
+                if constexpr (F8)
+                    load8_chunk(ul, c, ul * BUF);
+                else
+                    load(ul, c, ul * BUF);
+            }
             load_scale_bytes(ul, ul);
         }
         us = 1;
