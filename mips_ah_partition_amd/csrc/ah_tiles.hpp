@@ -228,7 +228,7 @@ __device__ __forceinline__ int here(int v) {
 template <int MODE, int OB>
 constexpr bool kPerm = OB == 2 && !p_by_col(MODE);
 template <int NP>
-constexpr int kTurnCols = NP == 2 ? 32 : 64;
+constexpr int kTurnCols = NP == 4 ? 64 : 32;
 template <int NP>
 constexpr int kTurnPitch = kTurnCols<NP> * 4 + 16;
 
@@ -402,47 +402,95 @@ __device__ __forceinline__ void dropout_factors(const Dropout& d, uint64_t step,
 // A dropped element is 0 whatever it was.
 __device__ __forceinline__ float dropped(float v, float f) { return f > 0.0f ? v * f : 0.0f; }
 
-// A wave's part of a gated product: a lane holds gate and up of the same columns, in fragments NP apart.
-template <int NQ, int NP, int OB>
+// Which of eight columns from j on (a multiple of 4; the second four are not asked for where it is none of 8) stay, as
+// 16-bit masks: u >= t where t - u, not below 0, is 0.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void keep_masks(const Dropout& d, uint64_t step, int32_t row, int32_t j, uint32_t* m) {
+    if (d.t == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m[q] = 0xFFFFFFFFu;
+        return;
+    }
+    const Philox u = philox(d, step, (uint32_t)row, (uint32_t)j >> 3);
+    const u16x2 t = {(unsigned short)d.t, (unsigned short)d.t}, one = {1, 1};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        m[q] = __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_elementwise_sub_sat(
+                                                t, __builtin_bit_cast(u16x2, u.w[q])), one) - one);
+    if (j & 4) {
+        m[0] = m[2];
+        m[1] = m[3];
+    }
+}
+// N values as bfloat16 under their masks, of which `left` exist.
+template <int N>
+__device__ __forceinline__ void put_masked(char* o, const float* v, const uint32_t* m, int32_t left, int32_t bypass) {
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) w[e] = (bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16) & m[e];
+    const v4i x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    if (left >= N) {
+        if constexpr (N == 8)
+            store16(o, x, bypass);
+        else
+            __builtin_memcpy(o, w, 2 * N);
+    } else if (left > 0) {
+        store_left<2>(o, x, left);
+    }
+}
+// Fragment row x of the sums.  A switch over a run-time x, so that what follows stands in the code once and not for every
+// x: unrolled the gated epilogues would outgrow the instruction cache.
+template <int FQ, int FP>
+__device__ __forceinline__ void take_row(v4f (&acc)[FQ][FP], int x, v4f (&t)[FP]) {
+#pragma unroll
+    for (int n = 0; n < FQ; ++n)
+        if (x == n) {
+#pragma unroll
+            for (int i = 0; i < FP * 4; ++i) {
+                if constexpr (FQ * FP > 16)
+                    t[i >> 2][i & 3] = acc_read(acc[n][i >> 2][i & 3]);
+                else
+                    asm volatile("v_mov_b32 %0, %1" : "=v"(t[i >> 2][i & 3]) : "v"(acc[n][i >> 2][i & 3]));
+            }
+        }
+}
+
+// A wave's part of a gated product: a lane holds gate and up of the same columns, in fragments NP apart.  The
+// activation is a template's, chosen once a tile: chosen for each element the compiler computes all and selects.  WHOLE:
+// all the tile's columns exist, so that nothing but the rows is asked about.
+template <int ACT, bool WHOLE, int NQ, int NP, int OB>
 __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ][2 * NP], const int32_t (&out_row)[2],
                                            int32_t j0, uint64_t step) {
     constexpr int FQ = 2 * NQ, Y = OB == 2 ? 2 : 1, N = 4 * Y;
     const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
     const int32_t jw = j0 + (wave & 1) * 16 * NP + g * N;
-#pragma unroll
+    const uint32_t all[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+#pragma nounroll
     for (int x = 0; x < FQ; ++x) {
-        const int32_t row = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+        const int32_t row = __shfl(x < 4 ? out_row[0] : out_row[1], (x & 3) * 16 + li, 64);
+        v4f t[2 * NP];
+        take_row(acc, x, t);
 #pragma unroll
         for (int y = 0; y < NP; y += Y) {
-            const int32_t j = jw + y * 16, left = (int32_t)a.J - j;
-            float u[N], v[N], f[N], h[N];
+            const int32_t j = jw + y * 16, left = WHOLE ? N : (int32_t)a.J - j;
+            float u[N], v[N], h[N];
+            uint32_t m[4];
+            keep_masks(a.drop, step, row, j, m);
 #pragma unroll
-            for (int s = 0; s < Y; ++s)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (NQ * NP > 4) {
-                        u[s * 4 + e] = acc_read(acc[x][y + s][e]);
-                        v[s * 4 + e] = acc_read(acc[x][y + NP + s][e]);
-                    } else {
-                        u[s * 4 + e] = acc[x][y + s][e];
-                        v[s * 4 + e] = acc[x][y + NP + s][e];
-                    }
-                }
-            dropout_factors<N>(a.drop, step, row, j, f);
-            if (a.act == AH_SILU) {
-#pragma unroll
-                for (int e = 0; e < N; ++e) h[e] = dropped(activate(AH_SILU, u[e]) * v[e], f[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) h[e] = dropped(activate(a.act, u[e]) * v[e], f[e]);
+            for (int e = 0; e < N; ++e) {
+                u[e] = t[y + e / 4][e & 3];
+                v[e] = t[y + NP + e / 4][e & 3];
+                h[e] = activate(ACT, u[e]) * v[e] * a.drop.factor;
             }
             if (row >= 0 && left > 0) {
                 if constexpr (OB == 2) {
-                    put_bf16<N>(static_cast<char*>(a.out) + (row * a.J + j) * 2, h, left);
+                    put_masked<N>(static_cast<char*>(a.out) + (row * a.J + j) * 2, h, m, left, a.bypass);
                 } else {
+                    v4i w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = m[e >> 1] >> (e & 1 ? 16 : 0) & 1 ? __builtin_bit_cast(int, h[e]) : 0;
                     char* const o = static_cast<char*>(a.out) + (row * a.J + j) * 4;
-                    const v4i w = {__builtin_bit_cast(int, h[0]), __builtin_bit_cast(int, h[1]),
-                                   __builtin_bit_cast(int, h[2]), __builtin_bit_cast(int, h[3])};
                     if (left >= 4)
                         __builtin_memcpy(o, &w, 16);
                     else
@@ -450,8 +498,8 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
                 }
                 if (a.pre) {
                     char* const o = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
-                    put_bf16<N>(o, u, left);
-                    put_bf16<N>(o + a.J * 2, v, left);
+                    put_masked<N>(o, u, all, left, a.bypass);
+                    put_masked<N>(o + a.J * 2, v, all, left, a.bypass);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -469,54 +517,65 @@ __device__ __forceinline__ void eight_columns(v4f f0, v4f f1, float* v) {
         v[4 + e] = __uint_as_float(t[1]);
     }
 }
-// A wave's part of the gradient: dh becomes (da, db) and h.  What the projections' loads take is hidden by asking for
-// the next fragment row's before this one's arithmetic.
-template <int NQ, int NP>
+// A wave's part of the gradient: dh becomes (da, db) and h.  The projections of fragment row x + 1 are asked for before
+// row x is dealt with; where the tile is WHOLE without a branch (rows that are not written read row 0), behind which the
+// compiler would wait for all of them.
+template <int ACT, bool WHOLE, int NQ, int NP>
 __device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ][2 * NP], const int32_t (&out_row)[2],
                                            int32_t leaf, int32_t j0, uint64_t step) {
-    static_assert(NQ * NP <= 4, "");
     constexpr int FQ = 2 * NQ, N = 8;
     const int tid = here(threadIdx.x), lane = tid & 63, wave = tid >> 6, g = lane >> 4, li = lane & 15;
     const int32_t jw = j0 + (wave & 1) * 32 * NP + (g & 1) * 16 + (g >> 1) * 8;
-    v4i u[2][NP], v[2][NP];
-    int32_t rows[2];
+    v4i u1[NP], v1[NP];
+    int32_t row1;
     auto ask = [&](int x) {
-        const int32_t row = rows[x & 1] = __shfl(out_row[x / 4], (x & 3) * 16 + li, 64);
+        row1 = __shfl(x < 4 ? out_row[0] : out_row[1], (x & 3) * 16 + li, 64);
+        const char* const p = a.pre + ((int64_t)(row1 < 0 ? 0 : row1) * 2 * a.J + jw) * 2;
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
-            const int32_t j = jw + z * 32, left = row < 0 ? 0 : (int32_t)a.J - j;
-            const char* const p = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
-            u[x & 1][z] = get_bf16x8(p, left);
-            v[x & 1][z] = get_bf16x8(p + a.J * 2, left);
+            const int32_t left = WHOLE ? N : row1 < 0 ? 0 : (int32_t)a.J - (jw + z * 32);
+            u1[z] = get_bf16x8(p + z * 64, left);
+            v1[z] = get_bf16x8(p + z * 64 + a.J * 2, left);
         }
     };
     ask(0);
-#pragma unroll
+#pragma nounroll
     for (int x = 0; x < FQ; ++x) {
-        if (x + 1 < FQ) ask(x + 1);
-        const int32_t row = rows[x & 1];
+        const int32_t row = row1;
+        v4i u[NP], v[NP];
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
-            const int32_t j = jw + z * 32, left = row < 0 ? 0 : (int32_t)a.J - j;
-            float f[N], dh[N], da[N], db[N], h[N];
-            eight_columns(acc[x][2 * z], acc[x][2 * z + 1], dh);
-            dropout_factors<N>(a.drop, step, row, j, f);
+            u[z] = u1[z];
+            v[z] = v1[z];
+        }
+        if (x + 1 < FQ) ask(x + 1);
+        v4f t[2 * NP];
+        take_row(acc, x, t);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int z = 0; z < NP; ++z) {
+            const int32_t j = jw + z * 32, left = row < 0 ? 0 : WHOLE ? N : (int32_t)a.J - j;
+            float dh[N], da[N], db[N], h[N];
+            uint32_t m[4];
+            eight_columns(t[2 * z], t[2 * z + 1], dh);
+            keep_masks(a.drop, step, row, j, m);
+            if (leaf < 0) m[0] = m[1] = m[2] = m[3] = 0;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const bool keep = f[e] > 0.0f && leaf >= 0;  // else all zero, whatever the projections hold
-                const float up = keep ? bf16_at(v[x & 1][z], e) * f[e] : 0.0f, d = keep ? dh[e] : 0.0f;
-                float t, dt;
-                activate_grad(a.act, keep ? bf16_at(u[x & 1][z], e) : 0.0f, &t, &dt);
-                da[e] = d * up * dt;
-                db[e] = d * t * f[e];
-                h[e] = t * up;
+                const float up = bf16_at(v[z], e), d = dh[e] * a.drop.factor;
+                float f, df;
+                activate_grad(ACT, bf16_at(u[z], e), &f, &df);
+                da[e] = d * up * df;
+                db[e] = d * f;
+                h[e] = f * up * a.drop.factor;
             }
             if (left > 0) {
                 char* const o = static_cast<char*>(a.out) + ((int64_t)row * 2 * a.J + j) * 2;
-                put_bf16<N>(o, da, left);
-                put_bf16<N>(o + a.J * 2, db, left);
-                if (a.hidden) put_bf16<N>(a.hidden + (row * a.J + j) * 2, h, left);
+                put_masked<N>(o, da, m, WHOLE ? N : left, a.bypass);
+                put_masked<N>(o + a.J * 2, db, m, WHOLE ? N : left, a.bypass);
+                if (a.hidden) put_masked<N>(a.hidden + (row * a.J + j) * 2, h, m, WHOLE ? N : left, a.bypass);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -575,9 +634,10 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 }
 
 // Tiles of NQ x NP blocks by a grid of resident workgroups, four waves each, a wave with a
-// quarter of the tile (32 NQ x 32 NP); OB bytes an output.  DMA: operands are 16-byte aligned with
+// quarter of the tile (32 NQ x 32 NP); OB bytes an output.  DMA 1: operands are 16-byte aligned with
 // whole chunks, and go straight to LDS; otherwise (2 x 2) chunks go through registers, where a
-// chunk's missing elements become zero.
+// chunk's missing elements become zero.  DMA 2 (gated): the sum is made of whole steps, two at least, and the row
+// side spans less than 4 GB, so that a chunk's address is a uniform one and a 32-bit offset that holds for the whole tile.
 //
 // Two LDS buffers, one sum step each, and two sets of fragments, 64 bytes of the sum each:
 //   first half of step G    multiplies the step's first fragments, reads its second ones
@@ -600,14 +660,16 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // TFLOP/s; zeros 2.40 GHz), with the LDS reads of a step 1661; the int8 kernel runs at 1.9 GHz, the bfloat16
 // one at 1.4 to 1.6.  Without the loads, the barrier or the wait for them (8192 x 6144 x 4096, bfloat16) 360, 422
 // and 442 us instead of 446, on zeros 337.
-template <int MODE, int NQ, int NP, int OB, bool DMA>
+template <int MODE, int NQ, int NP, int OB, int DMA>
 __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(ProdArgs a) {
     constexpr int ELEM = elem_bytes(MODE), FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
     constexpr bool QCOL = MODE == kDw, PCOL = p_by_col(MODE), RAGGED = is_ragged(MODE), PLAIN = is_plain(MODE);
-    constexpr bool PERM = kPerm<MODE, OB>, GATE = MODE == kGate, F8 = is_f8(MODE);
+    constexpr bool PERM = kPerm<MODE, OB>, GATE = MODE == kGate, F8 = is_f8(MODE), FAST = DMA == 2;
     constexpr int TQ = NQ * 64, TP = NP * 64 / (GATE ? 2 : 1), STEP = 128 / ELEM;
     constexpr int BUF = NB * kBlock;
-    constexpr int QR = QCOL ? 2 : PLAIN ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : 2 * NQ;
+    // Rows that a thread loads of a row operand's 64, in how many loads: FAST one of 16 bytes of 64, else two of 128.
+    constexpr int RH = FAST ? 64 : 32, QS = FAST ? NQ : 2 * NQ;
+    constexpr int QR = QCOL ? 2 : PLAIN || FAST ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : QS;
     __shared__ __align__(1024) char lds[(DMA ? 2 : 1) * BUF];
     __shared__ __align__(16) char turns[OB == 4 && !GATE ? 4 * 16 * kTurnPitch<NP> : 16];
     __shared__ __align__(16) float scales[MODE == kI8 ? 128 * NP + 64 * NQ : F8 ? 64 * NP : 4];
@@ -704,12 +766,15 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     auto ckey = [](int r) { return ((r >> 1) & 1) | ((r >> 3) & 1) << 1; };
     const int rr = tid >> 3, rc = ((tid & 7) ^ key(rr)) * 16;
     const int cc = ((((tid & 7) >> 1) ^ ckey(rr)) << 1 | (tid & 1)) * 16;
+    // FAST: rows of 64 bytes, chunk c at c ^ turn(row / 4), of PERM column rows (8 a + b) c ^ turn(row / 8).  Of lanes 0-3,
+    // 12-15, 20-23 and 24-27 each four rows fill 256 bytes but for the chunk, so turn has to give them four: 0, 3, 2, 1.
+    auto turn4 = [](int r) { return -r & 3; };
 
     Tile w;                               // the tile that is loaded
     const char* qrow[QR];                 // row operand: its rows; by column: this step's memory rows
     const char* prow[MODE == kDw || GATE ? 2 : 1];
-    uint32_t poff[PCOL ? 1 : GATE ? NP : 2 * NP];  // rows that follow one another: offsets from prow[0], qrow[0]
-    uint32_t qoff[PLAIN ? 2 * NQ : 1];
+    uint32_t poff[PCOL ? (FAST ? NP : 1) : GATE ? (FAST ? NP / 2 : NP) : 2 * NP];  // rows that follow one another: offsets
+    uint32_t qoff[PLAIN ? 2 * NQ : FAST ? NQ : 1];  // from prow[0], qrow[0] (FAST: of the blocks, of the rows from a.q)
     int32_t slot[SLOTS];                  // slots of a tile's rows; dw: of the next step's memory rows
 
     // What the order holds is kept as it was read until it is used, a step later: a check beside the
@@ -741,23 +806,23 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // this wave's part, where the results go), later the addresses.
     auto take_rows = [&](const Tile& n, int32_t(&rows)[2]) {
         if constexpr (RAGGED) {
-            const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7, rr = tid >> 3;
+            const int tid = here(threadIdx.x), lane = tid & 63, wq = tid >> 7, rr = tid / (256 / RH);
             const int32_t some = n.p0 < a.T ? n.p0 : 0;  // rows past the tile repeat its first
-            int32_t in[2 * NQ + 2];
+            int32_t in[QS + 2];
 #pragma unroll
-            for (int s = 0; s < 2 * NQ + 2; ++s) {
-                const int32_t r = n.p0 + (s < 2 * NQ ? s * 32 + rr : wq * 32 * NQ + (s - 2 * NQ) * 64 + lane);
+            for (int s = 0; s < QS + 2; ++s) {
+                const int32_t r = n.p0 + (s < QS ? s * RH + rr : wq * 32 * NQ + (s - QS) * 64 + lane);
                 in[s] = r < n.p1 ? r : some;
             }
 #pragma unroll
-            for (int s = 0; s < 2 * NQ; ++s) slot[s] = in[s];
+            for (int s = 0; s < QS; ++s) slot[s] = in[s];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) rows[u] = in[2 * NQ + u];
+            for (int u = 0; u < 2; ++u) rows[u] = in[QS + u];
             if (a.order) {
 #pragma unroll
-                for (int s = 0; s < 2 * NQ; ++s) slot[s] = a.order[in[s]];
+                for (int s = 0; s < QS; ++s) slot[s] = a.order[in[s]];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) rows[u] = a.order[in[2 * NQ + u]];
+                for (int u = 0; u < 2; ++u) rows[u] = a.order[in[QS + u]];
             }
         }
     };
@@ -776,7 +841,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         }
     };
     auto set_addresses = [&]() {
-        const int rr = here(tid) >> 3;
+        const int rr = here(tid) >> 3, r4 = here(tid) >> 2;
         if constexpr (PLAIN) {
             qrow[0] = a.q + w.p0 * a.qs + (F8 ? 0 : rc);
 #pragma unroll
@@ -786,15 +851,26 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
         } else if constexpr (!QCOL) {
 #pragma unroll
-            for (int s = 0; s < 2 * NQ; ++s) {
+            for (int s = 0; s < QS; ++s) {
                 int32_t r = known(slot[s]) ? slot[s] : 0;
                 if constexpr (MODE == kFwd || GATE) r = (int32_t)query_of(a, (uint32_t)r);
-                qrow[s] = a.q + (int64_t)r * a.qs + rc;
+                if constexpr (FAST)  // (a tile without a sum is loaded from zero_rows)
+                    qoff[s] = (w.red > 0 ? (uint32_t)((int64_t)r * a.qs) : 0u) + (((tid & 3) ^ turn4(r4 >> 2)) * 16);
+                else
+                    qrow[s] = a.q + (int64_t)r * a.qs + rc;
             }
         }
         const char* pbase = a.p + (RAGGED && w.leaf > 0 ? w.leaf * a.pg : 0);
-        if constexpr (GATE) {
-            // Rows of the tile: for each of the wave's columns' halves, 16 NP gate rows, then their up rows.
+        if constexpr (GATE && FAST) {
+            // blocks: the gate rows of the tile's columns, then their up rows
+            prow[0] = pbase + w.j0 * a.ps;
+            prow[1] = prow[0] + a.J * a.ps;
+#pragma unroll
+            for (int s = 0; s < NP / 2; ++s)
+                poff[s] = (w.j0 + s * 64 + r4 < a.J && w.red > 0 ? (uint32_t)((s * 64 + r4) * a.ps) : 0u) +
+                          (((tid & 3) ^ turn4(PERM ? r4 >> 3 : r4 >> 2)) * 16);
+        } else if constexpr (GATE) {
+            // rows of the tile: for each of the wave's columns' halves, 16 NP gate rows, then their up rows
             prow[0] = pbase + w.j0 * a.ps + rc;
             prow[1] = prow[0] + a.J * a.ps;
 #pragma unroll
@@ -810,6 +886,11 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                 // (a step past the sum of float8 rows comes from zero_rows: rows of one step, or a tile of nothing)
                 poff[s] = (w.j0 + r < a.J && (!F8 || w.red > 0) ? (uint32_t)(r * a.ps) : 0u) + (F8 ? rc : 0);
             }
+        } else if constexpr (FAST) {
+            prow[0] = pbase + (int64_t)w.j0 * 2;
+#pragma unroll
+            for (int h = 0; h < NP; ++h)  // columns past the last repeat the tile's first; they are not written
+                poff[h] = w.red > 0 ? (uint32_t)(rr * a.ps) + (w.j0 + h * 64 + cc / 2 < a.J ? h * 128 + cc : 0) : cc;
         } else if constexpr (MODE != kDw) {
             prow[0] = pbase + rr * a.ps + (int64_t)w.j0 * 2 + cc;
         }
@@ -857,6 +938,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // instruction: lane 16 g + i holds bytes 16 g .. 16 g + 15 of row i.  By column that is eight
     // summed rows, two transposed reads of four.
     const uint32_t base = lds_addr(lds);
+    const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(base + wave * 1024);
     // PERM: row 4 a + b of column fragment y is column 32 (y / 2) + 8 a + 4 (y & 1) + b of the part, so
     // that fragments 2 z and 2 z + 1 leave eight consecutive columns in a lane.
     const int pl = PERM ? (li >> 2) * 8 + (li & 3) : li;
@@ -939,6 +1021,60 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         const char* src = source(u, c, &valid, &before);
         dma16(valid > 0 ? src : zero, base + buf + c * 4096 + wave * 1024);
     };
+    // FAST.  LDS is a ring of four half-steps (64 bytes of the sum: 4 KB a block).  Half-step h is multiplied from registers
+    // while h + 1 is read from the ring and the loads of h + 4 go where h was, so that a load has two to three half-steps to
+    // arrive, where two buffers of whole steps give it one to two (the wait for them was a third of the loop: 410 us of
+    // 16,384 rows x 1536 -> 2 x 4096 without a store, 265 without the loads).  One read or one load stands between two
+    // matrix instructions; column fragments are read first, since the next half's first FP instructions use all of them.
+    constexpr uint32_t SLOT = NB * 4096;
+    const uint32_t qring = base + NP * 4096 + (wq * 32 * NQ + li) * 64 + ((g ^ turn4(li >> 2)) * 16);
+    const uint32_t pring = base + (wp * 16 * NP + pl) * 64 + ((g ^ turn4(li >> 2)) * 16);
+    uint32_t cring[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) cring[n] = base + (tr * 128 + ((n ^ ckey(tr)) * 32) + (li & 3) * 8);
+    auto ring_q = [&](int x, uint32_t at) -> v4i { return by_row(qring + at, x * 1024); };
+    auto ring_p = [&](int y, uint32_t at) -> v4i {
+        if constexpr (PCOL) {
+            const int n = NP == 2 ? y : y & 3;  // fragment wp FP + y: block / 4, granule & 3
+            return by_col(cring[n & 3] + at + wp * (FP / 4) * 4096, (y >> 2) * 4096);
+        } else {
+            const int h = y / NP, f = y % NP;  // gate or up, fragment
+            return by_row(pring + at, h * (NP / 2) * 4096 + (PERM ? (f >> 1) * 2048 + (f & 1) * 256 : f * 1024));
+        }
+    };
+    auto ring_load = [&](int u, int half, int c, uint32_t at) {
+        if constexpr (FAST) {
+            const char* src;
+            uint32_t off;
+            if (c >= NP) {
+                src = a.q + u * 128 + half * 64;
+                off = qoff[c - NP];
+            } else if constexpr (GATE) {
+                src = prow[c / (NP / 2)] + u * 128 + half * 64;
+                off = poff[c % (NP / 2)];
+            } else {
+                src = prow[0] + ((int64_t)u * 64 + half * 32) * a.ps;
+                off = poff[c];
+            }
+            dma16(u * 64 < w.red ? src : reinterpret_cast<const char*>(zero_rows), off, lds_wave + at + c * 4096);
+        }
+    };
+    auto half_ring = [&](int kk, uint32_t from, uint32_t to, int u) {
+        constexpr int NM = FQ * FP, NR = FQ + FP;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            acc[m / FP][m % FP] = mma<MODE>(pf[kk][m % FP], qf[kk][m / FP], acc[m / FP][m % FP]);
+            const int r = (2 * m * NR + NM - 1) / NM, c = m * NB / NM;  // at most one read (in the first half) and one load
+            if (r < NR && r * NM / (2 * NR) == m) {
+                if (r >= 1 && r <= FP)
+                    pf[kk ^ 1][r - 1] = ring_p(r - 1, from);
+                else
+                    qf[kk ^ 1][r ? r - FP : 0] = ring_q(r ? r - FP : 0, from);
+            }
+            if (c < NB && c * NM / NB + NM / (2 * NB) == m) ring_load(u, kk, c, to);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
     // One half-step: the matrix instructions of fragment set kk; between them the reads of
     // the other set from `buf` and (kk = 1) the loads of step u into the other buffer.
     // float8: half-step kk multiplies half of the row fragments with all column fragments; the first reads the other half,
@@ -946,7 +1082,6 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // instructions (32 clocks) stands one load or one fragment's reads: in a lump behind every fourth they cost the
     // pipe (8192 x 4096 x 16384: 627 us with them).  So that a load is three instructions its address is a uniform one
     // and a lane's offset, the same all along a tile.
-    const uint32_t lds_wave = __builtin_amdgcn_readfirstlane(base + wave * 1024);
     auto load8_chunk = [&](int u, int c, uint32_t buf) {
         if constexpr (F8) {
             const bool in = u * STEP < w.red;
@@ -1036,11 +1171,26 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 
     const uint64_t call_step = is_gated(MODE) && a.drop.t ? step_of_call(a.drop) : 0;
     auto store = [&](const int32_t(&rows)[2], const Tile& n) {
-        if constexpr (GATE)
-            store_gate<NQ, NP, OB>(a, acc, rows, n.j0, call_step);
-        else if constexpr (MODE == kGrad)
-            store_grad<NQ, NP>(a, acc, rows, n.leaf, n.j0, call_step);
-        else
+        if constexpr (is_gated(MODE)) {
+            auto with = [&](auto act, auto whole) {
+                if constexpr (GATE)
+                    store_gate<decltype(act)::value, decltype(whole)::value, NQ, NP, OB>(a, acc, rows, n.j0, call_step);
+                else
+                    store_grad<decltype(act)::value, decltype(whole)::value, NQ, NP>(a, acc, rows, n.leaf, n.j0, call_step);
+            };
+            auto for_act = [&](auto act) {
+                if (n.j0 + TP <= a.J)
+                    with(act, std::true_type());
+                else
+                    with(act, std::false_type());
+            };
+            if (a.act == AH_SILU)
+                for_act(std::integral_constant<int, AH_SILU>());
+            else if (a.act == AH_GELU)
+                for_act(std::integral_constant<int, AH_GELU>());
+            else
+                for_act(std::integral_constant<int, AH_RELU>());
+        } else
             store_part<MODE, NQ, NP, OB>(a, acc, scales, turns + (OB == 4 ? wave * 16 * kTurnPitch<NP> : 0), rows, n.leaf, n.j0);
     };
     int64_t t = tbeg + (blockIdx.x >> 3);
@@ -1088,6 +1238,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             for (int c = 0; c < 2 * NB; ++c) {
                 if constexpr (F8)
                     load8_chunk(ul, c, ul * BUF);
+                else if constexpr (FAST)
+                    ring_load(ul, c / NB, c % NB, (2 * ul + c / NB) * SLOT);
                 else
                     load(ul, c, ul * BUF);
             }
@@ -1100,8 +1252,13 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 #pragma unroll
         for (int u = 0; u < 2; ++u) rows_c[u] = rows_l[u];
         clear();
-        land<2 * NB>();  // (float8: a wave has up to one more of step 1 in flight)
-        if constexpr (F8) {
+        land<FAST ? 3 * NB : 2 * NB>();  // (float8: a wave has up to one more of step 1 in flight)
+        if constexpr (FAST) {
+#pragma unroll
+            for (int x = 0; x < FQ; ++x) qf[0][x] = ring_q(x, 0);
+#pragma unroll
+            for (int y = 0; y < FP; ++y) pf[0][y] = ring_p(y, 0);
+        } else if constexpr (F8) {
 #pragma unroll
             for (int x = 0; x < FQ / 2; ++x) read_q8(0, x, 0);
 #pragma unroll
@@ -1117,11 +1274,15 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             if constexpr (PLAIN) {
                 if (uc == 0) load_scales(wc, sv);
             }
-            if constexpr (F8)
+            if constexpr (FAST) {
+                land<2 * NB>();  // half-step 1 of this step is there; two are in flight
+            } else if constexpr (F8) {
                 half_step8(0, cur, 0);
-            else
+                land<0>();
+            } else {
                 half_step(0, cur, 0);
-            land<0>();
+                land<0>();
+            }
             if constexpr (PLAIN) {
                 if (uc == 0) keep_scales(sv);
             }
@@ -1134,12 +1295,17 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
             if constexpr (MODE == kDw) set_rows(ul, slot);
             advance_order();
-            if constexpr (F8)
+            if constexpr (F8) {
                 half_step8(1, BUF - cur, ul++);
-            else
+            } else if constexpr (FAST) {  // cur: the half-steps of this step, in LDS at cur and cur + SLOT
+                half_ring(0, cur + SLOT, cur, ul);
+                land<2 * NB>();
+                half_ring(1, BUF - cur, cur + SLOT, ul++);
+            } else {
                 half_step(1, BUF - cur, ul++);
+            }
             if (++uc < wc.nt) continue;
-            if constexpr (NQ * NP > 4) settle();
+            if constexpr (NQ * NP > 4 || is_gated(MODE)) settle();
             out_rows(wc, rows_c);
             store(rows_c, wc);
             t += hop;
@@ -1196,6 +1362,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                 }
             }
             out_rows(w, rows);
+            if constexpr (is_gated(MODE)) settle();
             store(rows, w);
             t += hop;
             if (t >= tend) break;
@@ -1508,12 +1675,34 @@ int tile_shape(const ProdArgs& a) {
         const int64_t J = MODE == kGate ? 2 * a.J : a.J;
         return (double)((row_tiles<MODE>(a, TQ, false) * ((J + TP - 1) / TP) + resident - 1) / resident) * round;
     };
-    const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / 0.97),
+    const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / (MODE == kGate ? 0.87 : 0.97)),
                  t2 = time(128, 128, 2 * kCUs, 8 / 0.85);
     return t2 <= t3 && t2 <= t4 ? 2 : t3 < t4 ? 3 : 4;
 }
 
-template <int MODE, int NQ, int NP, bool DMA>
+// The same for float8, whose gradients have few tiles and long sums, so that the shape that fills the chip's
+// rounds best wins: 10 NQ + NP.  Rates relative to 4 x 4 on large products.
+template <int MODE>
+int f8_shape(const ProdArgs& a) {
+    const struct {
+        int nq, np, per_cu;
+        double rate;
+    } shapes[] = {{4, 4, 1, 1.0}, {3, 4, 1, 0.97}, {4, 3, 1, 0.97}, {2, 3, 1, 0.9}, {2, 2, 2, 0.85}};
+    int best = 0;
+    double least = 0.0;
+    for (const auto& s : shapes) {
+        const int64_t tiles = row_tiles<MODE>(a, s.nq * 64, false) * ((a.J + s.np * 64 - 1) / (s.np * 64)),
+                      resident = kCUs * s.per_cu;
+        const double time = (double)((tiles + resident - 1) / resident) * s.nq * s.np * s.per_cu / s.rate;
+        if (best == 0 || time < least) {
+            best = s.nq * 10 + s.np;
+            least = time;
+        }
+    }
+    return best;
+}
+
+template <int MODE, int NQ, int NP, int DMA>
 hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
     constexpr int TQ = NQ * 64, TP = NP * 64 / (MODE == kGate ? 2 : 1);
     const int64_t np = (a.J + TP - 1) / TP, each = row_tiles<MODE>(a, TQ, true) * np;
@@ -1525,7 +1714,7 @@ hipError_t launch_tiles(const ProdArgs& a, hipStream_t stream) {
     }
     if ((MODE != kDw || wgs * kNT > kMaxGridItems) && wgs > resident) wgs = resident;
     const dim3 grid((uint32_t)wgs);
-    if constexpr (MODE != kGrad) {
+    if constexpr (MODE != kGrad && !(MODE == kGate && NQ == 4)) {
         if (a.out_f32) {
             hipLaunchKernelGGL((prod_tile_kernel<MODE, NQ, NP, 4, DMA>), grid, dim3(kNT), 0, stream, a);
             return hipGetLastError();
@@ -1580,7 +1769,9 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     a.fan_shift = 31 + l;
     a.fan_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + fan - 1) / fan);
     const int64_t pitch = a.J * (a.out_f32 ? 4 : 2);
-    a.bypass = MODE != kFwd && MODE != kGate && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
+    uintptr_t sectors = reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch;
+    if (is_gated(MODE)) sectors |= reinterpret_cast<uintptr_t>(a.pre) | reinterpret_cast<uintptr_t>(a.hidden);
+    a.bypass = MODE != kFwd && !is_gated(MODE) && (sectors & 63) == 0;
     if constexpr (MODE == kI8 || MODE == kFwd || MODE == kGate) {
         switch (row_fragments<MODE>(a)) {
             case 1: return launch_rows<MODE, 1>(a, whole, stream);
@@ -1589,15 +1780,35 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
         }
     }
     if constexpr (!is_f8(MODE)) {
-        if (!whole) return launch_tiles<MODE, 2, 2, false>(a, stream);
+        if (!whole) return launch_tiles<MODE, 2, 2, 0>(a, stream);
     }
-    if constexpr (MODE == kDw || MODE == kGrad) {
-        return launch_tiles<MODE, 2, 2, true>(a, stream);
+    if constexpr (MODE == kDw) {
+        return launch_tiles<MODE, 2, 2, 1>(a, stream);
+    } else if constexpr (is_gated(MODE)) {
+        // Other sums (and more than 4 GB of rows) take the general loads, at the smallest tile.
+        if (a.red % 64 != 0 || a.red < 128 || a.T / fan * a.qs >= ((int64_t)1 << 32))
+            return launch_tiles<MODE, 2, 2, 1>(a, stream);
+        switch (tile_shape<MODE>(a)) {
+            case 4:
+                if constexpr (MODE == kGate) {  // float32 results would spill registers at 4 x 4
+                    if (!a.out_f32) return launch_tiles<MODE, 4, 4, 2>(a, stream);
+                }
+            case 3: return launch_tiles<MODE, 3, 4, 2>(a, stream);
+            default: return launch_tiles<MODE, 2, 2, 1>(a, stream);  // (with the ring's barriers 12 % slower)
+        }
+    } else if constexpr (is_f8(MODE)) {
+        switch (f8_shape<MODE>(a)) {
+            case 44: return launch_tiles<MODE, 4, 4, 1>(a, stream);
+            case 34: return launch_tiles<MODE, 3, 4, 1>(a, stream);
+            case 43: return launch_tiles<MODE, 4, 3, 1>(a, stream);
+            case 23: return launch_tiles<MODE, 2, 3, 1>(a, stream);
+            default: return launch_tiles<MODE, 2, 2, 1>(a, stream);
+        }
     } else {
         switch (tile_shape<MODE>(a)) {
-            case 4: return launch_tiles<MODE, 4, 4, true>(a, stream);
-            case 3: return launch_tiles<MODE, 3, 4, true>(a, stream);
-            default: return launch_tiles<MODE, 2, 2, true>(a, stream);
+            case 4: return launch_tiles<MODE, 4, 4, 1>(a, stream);
+            case 3: return launch_tiles<MODE, 3, 4, 1>(a, stream);
+            default: return launch_tiles<MODE, 2, 2, 1>(a, stream);
         }
     }
 }
