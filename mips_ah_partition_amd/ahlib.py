@@ -10,6 +10,7 @@ loudly.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -889,10 +890,11 @@ def _call(name, where, *args):
     _check(status, name)
 
 
-def _together(where, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != where.get_device():
-            raise ValueError(f"{name} is on another device")
+def _together(where, *tensors):
+    dev = where.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
 
 
 def _act_code(act):
@@ -929,7 +931,7 @@ def ah_grouped_gated(x, w, offsets=None, order=None, fan=1, act="silu", drop=0.0
     slots, n = m * fan, n2 // 2
     _leaf_starts(offsets, order, fan, slots, L)
     _count(step)
-    _together(x, w=w, offsets=offsets, order=order, step=step, out=out, pre_out=pre_out)
+    _together(x, w, offsets, order, step, out, pre_out)
     dtype = out_dtype if out is None else out.dtype
     odt = _float_code(dtype, "out")
     out = _out(out, (slots, n), dtype, "out", x.device, stream)
@@ -954,7 +956,7 @@ def ah_grouped_gated_grad(dy, w, pre, offsets=None, order=None, act="silu", drop
         raise ValueError("w and pre must have the widths of dy and of the block")
     _leaf_starts(offsets, order, 1, slots, L)
     _count(step)
-    _together(dy, w=w, pre=pre, offsets=offsets, order=order, step=step, dpre_out=dpre_out, hidden_out=hidden_out)
+    _together(dy, w, pre, offsets, order, step, dpre_out, hidden_out)
     dpre_out = _out(dpre_out, (slots, 2 * n), torch.bfloat16, "dpre_out", dy.device, stream)
     if hidden_out is not None or want_hidden:
         hidden_out = _out(hidden_out, (slots, n), torch.bfloat16, "hidden_out", dy.device, stream)
@@ -985,7 +987,7 @@ def ah_f8_quantize(x, dtype=torch.float8_e4m3fn, want_rows=True, want_columns=Fa
     x, xs = _rows(x, None, "x")
     dt, code = _float_code(x.dtype, "x"), _f8_code(dtype, "dtype")
     n, d = x.shape
-    _together(x, codes_out=codes_out, scale_out=scale_out, codes_t_out=codes_t_out, scale_t_out=scale_t_out)
+    _together(x, codes_out, scale_out, codes_t_out, scale_t_out)
     if want_rows or codes_out is not None:
         cs, ss = _f8_shapes(n, d)
         codes_out = _out(codes_out, cs, dtype, "codes_out", x.device, stream)
@@ -1004,9 +1006,9 @@ def _f8_operand(codes, scale, name):
         raise TypeError(f"{name} must be a device tensor")
     code = _f8_code(codes.dtype, name)
     _is(codes, codes.dtype, name, 2)
-    _is(scale, torch.uint8, f"{name}'s scale", 2)
+    _is(scale, torch.uint8, "the scale of codes", 2)
     n, kp = codes.shape
-    if kp % 128 or tuple(scale.shape) != _f8_shapes(n, kp)[1]:
+    if kp & 127 or scale.shape != (kp >> 7, (n + 15) & -16):
         raise ValueError(f"{name} and its scale must have the shapes that ah_f8_quantize gives")
     return code, n, kp
 
@@ -1024,7 +1026,7 @@ def ah_f8_matmul(x8, x_scale, w8, w_scale, bias=None, out_dtype=torch.bfloat16, 
     if kw != k:
         raise ValueError("w8 and x8 differ in their width")
     _f8_bias(bias, n)
-    _together(x8, x_scale=x_scale, w8=w8, w_scale=w_scale, bias=bias, out=out)
+    _together(x8, x_scale, w8, w_scale, bias, out)
     dtype = out_dtype if out is None else out.dtype
     odt = _float_code(dtype, "out")
     out = _out(out, (m, n), dtype, "out", x8.device, stream)
@@ -1036,6 +1038,7 @@ def ah_f8_matmul(x8, x_scale, w8, w_scale, bias=None, out_dtype=torch.bfloat16, 
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def ah_f8_linear_workspace_bytes(m: int, k: int) -> int:
     return int(lib().ah_f8_linear_workspace_bytes(m, k))
 
@@ -1051,7 +1054,7 @@ def ah_f8_linear(x, w8, w_scale, bias=None, x_type=torch.float8_e4m3fn, out_dtyp
     if kw != (k + 127) // 128 * 128:
         raise ValueError("w8 and x differ in their width")
     _f8_bias(bias, n)
-    _together(x, w8=w8, w_scale=w_scale, bias=bias, out=out, workspace=workspace)
+    _together(x, w8, w_scale, bias, out, workspace)
     dtype = out_dtype if out is None else out.dtype
     odt = _float_code(dtype, "out")
     out = _out(out, (m, n), dtype, "out", x.device, stream)
@@ -1080,7 +1083,7 @@ def ah_dropout(x, p, seed, step=None, residual=None, out=None, stream=None):
         if out.shape != x.shape:
             raise ValueError("out must have the shape of x")
     _count(step)
-    _together(x, step=step, residual=residual, out=out)
+    _together(x, step, residual, out)
     _call("ah_dropout", x, _at(x), dt, rows, n, xs, float(p), int(seed) & (2 ** 64 - 1), _at(step), _at(residual), rs,
           _at(out), os_, _on(stream, x))
     return out

@@ -1433,18 +1433,21 @@ __device__ __forceinline__ float step_of(float m) { return m < INFINITY ? m / 12
 // in 34 us for grouping and product (5.6 TB/s); one token, 1536 -> 4096, 9.5 us a call, a launch's
 // latency (7.0 on the GPU; 15.6 with tiles and quantising in a launch of its own).
 constexpr int kRowWaves = 8;
-template <int MODE, int FR, bool WHOLE, int XB>
+// STRIP (gated sums of at most 512 bytes, eight pieces): nothing to share out, so every wave has 16 columns of its own and the
+// whole sum (999 slots of 37 leaves, 100 -> 2 x 385: 18 us with the sum shared by eight waves).
+template <int MODE, int FR, bool WHOLE, int XB, bool STRIP = false>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
-    constexpr int ELEM = elem_bytes(MODE), U = 4, G = MODE == kGate ? 2 : 1;
+    constexpr int ELEM = elem_bytes(MODE), U = STRIP ? 2 : 4, G = MODE == kGate ? 2 : 1;
     static_assert(XB == 0 || (MODE == kI8 && FR == 1 && WHOLE), "");
     typedef typename Acc<MODE>::type acc_t;
-    __shared__ acc_t part[kRowWaves][G * FR][64];
+    __shared__ acc_t part[STRIP ? 1 : kRowWaves][STRIP ? 1 : G * FR][64];
     __shared__ float most[kRowWaves][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, li = lane & 15;
     const int32_t kb = (int32_t)a.red * ELEM, steps = (kb + 63) >> 6;
-    const int32_t s0 = steps * wave / kRowWaves, s1 = steps * (wave + 1) / kRowWaves;
-    const int32_t j = blockIdx.x * 16 + g * 4;  // this lane's four output columns
+    const int32_t s0 = STRIP ? 0 : steps * wave / kRowWaves, s1 = STRIP ? steps : steps * (wave + 1) / kRowWaves;
+    const int32_t strip = STRIP ? blockIdx.x * kRowWaves + wave : blockIdx.x;
+    const int32_t j = strip * 16 + g * 4;  // this lane's four output columns
     const int32_t leaf = MODE == kI8 ? 0 : blockIdx.y;
     const uint64_t call_step = MODE == kGate && a.drop.t ? step_of_call(a.drop) : 0;
     auto put = [&](int32_t row, v4f v) {
@@ -1473,8 +1476,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
     } else {  // rows of no leaf
         if (blockIdx.z > 0) return;
         const int32_t head = leaf_start(a, 0), tail = leaf_start(a, a.L);
-        for (int32_t p = tid >> 2; p < head + (int32_t)a.T - tail; p += kRowWaves * 16) {
-            const int32_t row = slot_of(a, p < head ? p : tail + p - head), c = blockIdx.x * 16 + (tid & 3) * 4;
+        for (int32_t p = (STRIP ? lane : tid) >> 2; p < head + (int32_t)a.T - tail; p += (STRIP ? 1 : kRowWaves) * 16) {
+            const int32_t row = slot_of(a, p < head ? p : tail + p - head), c = strip * 16 + (tid & 3) * 4;
             if (row < 0 || c >= a.J) continue;
             const int32_t left = (int32_t)a.J - c, ob = a.out_f32 ? 4 : 2;
             char* o = static_cast<char*>(a.out) + (row * a.J + c) * ob;
@@ -1488,7 +1491,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
         }
         return;
     }
-    const int32_t col = blockIdx.x * 16 + li < a.J ? blockIdx.x * 16 + li : (int32_t)a.J - 1;
+    if (STRIP && strip * 16 >= a.J) return;
+    const int32_t col = strip * 16 + li < a.J ? strip * 16 + li : (int32_t)a.J - 1;
     const char* const prow = a.p + leaf * a.pg + col * a.ps;
     auto fetch = [&](const char* row, int32_t o) -> v4i {
         v4i v = {0, 0, 0, 0};
@@ -1611,15 +1615,22 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                     }
                 }
         }
+        if constexpr (!STRIP) {
 #pragma unroll
-        for (int f = 0; f < G * FR; ++f) part[wave][f][lane] = acc[f];
-        __syncthreads();
+            for (int f = 0; f < G * FR; ++f) part[wave][f][lane] = acc[f];
+            __syncthreads();
+        }
+        auto sum_of = [&](int f) {
+            if constexpr (STRIP) return acc[f];
+            acc_t t = part[0][STRIP ? 0 : f][lane];
+#pragma unroll
+            for (int w = 1; w < kRowWaves; ++w) t += part[STRIP ? 0 : w][STRIP ? 0 : f][lane];
+            return t;
+        };
 #pragma unroll
         for (int f = 0; f < FR; ++f)
-            if (wave == f && out_row[f] >= 0) {
-                acc_t t = part[0][f][lane];
-#pragma unroll
-                for (int w = 1; w < kRowWaves; ++w) t += part[w][f][lane];
+            if ((STRIP || wave == f) && out_row[f] >= 0) {
+                const acc_t t = sum_of(f);
                 v4f v;
                 if constexpr (MODE == kI8) {
 #pragma unroll
@@ -1628,9 +1639,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                         if (a.bias) v[e] += bias[e];
                     }
                 } else if constexpr (G == 2) {
-                    v4f up = part[0][FR + f][lane];
-#pragma unroll
-                    for (int w = 1; w < kRowWaves; ++w) up += part[w][FR + f][lane];
+                    const v4f up = sum_of(FR + f);
                     float drop[4];
                     dropout_factors<4>(a.drop, call_step, out_row[f], j, drop);
 #pragma unroll
@@ -1646,7 +1655,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                 }
                 put(out_row[f], v);
             }
-        if (p + (int32_t)gridDim.z * 16 * FR < p1) __syncthreads();
+        if (!STRIP && p + (int32_t)gridDim.z * 16 * FR < p1) __syncthreads();
     }
 }
 
@@ -1743,6 +1752,14 @@ hipError_t launch_rows(const ProdArgs& a, bool whole, hipStream_t stream) {
     // a leaf's rows beyond 16 FR go to a second workgroup
     const dim3 grid((uint32_t)((a.J + 15) / 16), (uint32_t)(MODE == kI8 ? (a.T + 16 * FR - 1) / (16 * FR) : a.L + 1),
                     MODE == kI8 || a.T / a.L < 8 ? 1 : 2);
+    if constexpr (MODE == kGate) {
+        if (a.red * 2 <= kRowWaves * 64) {
+            const dim3 strips((grid.x + kRowWaves - 1) / kRowWaves, grid.y, grid.z);
+            auto kernel = whole ? prod_rows_kernel<MODE, FR, true, 0, true> : prod_rows_kernel<MODE, FR, false, 0, true>;
+            hipLaunchKernelGGL(kernel, strips, dim3(kRowWaves * 64), 0, stream, a);
+            return hipGetLastError();
+        }
+    }
     if constexpr (XB == 0) {
         if (!whole) {
             hipLaunchKernelGGL((prod_rows_kernel<MODE, FR, false, 0>), grid, dim3(kRowWaves * 64), 0, stream, a);
