@@ -1,0 +1,71 @@
+"""The large tile shapes of the gated products (256 x 256, 192 x 256), which only batches of thousands of rows reach: their ring
+of half-steps, and dropout's numbers made in the loop where the sum has many steps and behind it where it has few.  References and
+tolerances as in test_gpu_gated.
+"""
+import pytest
+
+from philox_reference import factors
+from test_gpu_gated import _act, _forward_reference, _half, _route, gpu  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# m, L, k, n: one leaf and several with ragged ends, 2 to 32 steps of 64, whole and partial columns
+CASES = [(16128, 1, 128, 512), (12096, 1, 128, 512), (15000, 3, 192, 500), (11300, 4, 320, 520), (12096, 1, 2048, 512), (16128, 1, 1600, 512),
+         (40000, 5, 256, 136)]
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25])
+@pytest.mark.parametrize("m,L,k,n", CASES)
+def test_forward(gpu, m, L, k, n, p):  # noqa: F811
+    torch, ah = gpu
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + L + k + n)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    act = ["silu", "gelu", "relu"][(m + n) % 3]
+    x, w = rnd(m, k).bfloat16(), (rnd(L, 2 * n, k) * k ** -0.5 * 2).bfloat16()
+    leaves, offsets, order = _route(torch, ah, rnd, m, 1, L, none=0.02 if L > 1 else 0)
+    factor = torch.from_numpy(factors(m, n, p, 77, 5)).cuda()
+    step = torch.tensor([5], device="cuda")
+    want, tol, wpre, epre = _forward_reference(torch, x, w, leaves, act, factor)
+    for dt in (torch.bfloat16, torch.float32):
+        big, bigp = torch.full((m + 1, n), 7.0, dtype=dt, device="cuda"), torch.full((m + 1, 2 * n), 7.0, device="cuda").bfloat16()
+        h, pre = ah.ah_grouped_gated(x, w, offsets, order=order, act=act, drop=p, seed=77, step=step, out=big[:m], pre_out=bigp[:m])
+        assert (big[m:] == 7).all() and (bigp[m:] == 7).all()
+        assert ((h.double() - want).abs() <= tol + (want.abs() + tol) * _half(torch, dt)).all()
+        assert ((pre.double() - wpre).abs() <= epre + (wpre.abs() + epre) * 2.0 ** -8).all()
+        assert (h[leaves.flatten() < 0] == 0).all() and (pre[leaves.flatten() < 0] == 0).all() and (h[factor == 0] == 0).all()
+        again, _ = ah.ah_grouped_gated(x, w, offsets, order=order, act=act, drop=p, seed=77, step=step, out_dtype=dt)
+        assert torch.equal(again, h)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25])
+@pytest.mark.parametrize("m,L,d,n", [(12096, 1, 128, 1024), (11300, 4, 320, 1000), (12096, 1, 1600, 1024), (30000, 5, 256, 264)])
+def test_gradient(gpu, m, L, d, n, p):  # noqa: F811
+    torch, ah = gpu
+    D = torch.float64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + L + d + n)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    act = ["silu", "gelu", "relu"][(m + d) % 3]
+    dy, w, pre = rnd(m, d).bfloat16(), (rnd(L, d, n) * n ** -0.5).bfloat16(), (rnd(m, 2 * n) * 2).bfloat16()
+    leaves, offsets, order = _route(torch, ah, rnd, m, 1, L, none=0.02 if L > 1 else 0)
+    flat = leaves.flatten()
+    factor = torch.from_numpy(factors(m, n, p, 3, 0)).cuda()
+    dpre, h = ah.ah_grouped_gated_grad(dy, w, pre, offsets, order=order, act=act, drop=p, seed=3)
+    over = pre.clone()
+    ah.ah_grouped_gated_grad(dy, w, over, offsets, order=order, act=act, drop=p, seed=3, want_hidden=False, dpre_out=over)
+    assert torch.equal(over, dpre)
+    dh, size = torch.zeros(m, n, dtype=D, device="cuda"), torch.zeros(m, n, dtype=D, device="cuda")
+    for l in range(L):
+        at = (flat == l).nonzero().flatten()
+        dh[at] = dy[at].to(D) @ w[l].to(D)
+        size[at] = dy[at].to(D).abs() @ w[l].to(D).abs()
+    a, b = pre.to(D).chunk(2, 1)
+    f, df = _act(torch, a, act)
+    e, ef, edf = (d + 16) * 2.0 ** -23 * size, (f.abs() * (a.abs() + 16) + a.abs()) * 2.0 ** -22, (a.abs() + 16) * 2.0 ** -22
+    dh = dh * factor
+    some = (flat >= 0)[:, None].to(D)
+    for got, want, tol in ((dpre[:, :n], dh * b * df, (e * (df.abs() + edf) * factor + dh.abs() * edf) * b.abs()),
+                           (dpre[:, n:], dh * f, e * (f.abs() + ef) * factor + dh.abs() * ef), (h, f * b * factor * some, ef * b.abs() * factor)):
+        assert ((got.double() - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8).all()
+    assert (dpre[flat < 0] == 0).all() and (h[flat < 0] == 0).all()
