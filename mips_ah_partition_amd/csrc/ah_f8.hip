@@ -107,20 +107,21 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(const T* x, int64_t n, int
 }
 
 // Columns to codes (the transposed matrix), and rows too where wanted, from one reading: a workgroup has 128 x 128
-// elements, its rows' blocks in registers, its columns' through LDS.
+// elements, its rows' blocks in registers, its columns' through LDS, 32 elements of a column a thread.
+constexpr int kColThreads = 512, kParts = kColThreads / kBlk, kPart = kBlk / kParts;
 template <typename T, int TYPE, bool WHOLE, bool ROWS>
-__global__ __launch_bounds__(256) void f8_columns_kernel(const T* x, int64_t n, int64_t d, int64_t xs, uint8_t* codes,
+__global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int64_t n, int64_t d, int64_t xs, uint8_t* codes,
                                                          uint8_t* scale, uint8_t* codes_t, uint8_t* scale_t) {
     __shared__ __align__(16) T tile[kBlk][kBlk + 8];
-    __shared__ float most[2][kBlk];
-    const int tid = threadIdx.x, lane = tid & 63;
+    __shared__ float most[kParts][kBlk];
+    const int tid = threadIdx.x;
     const int64_t kb = (d + kBlk - 1) / kBlk, nb = (n + kBlk - 1) / kBlk;
     const int64_t pitch = (n + 15) / 16 * 16, pitch_t = (d + 15) / 16 * 16;
     for (int64_t i = blockIdx.x; i < kb * nb; i += gridDim.x) {
         const int64_t r0 = i / kb * kBlk, b = i % kb, c0 = b * kBlk, c = c0 + (tid & 15) * 8;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int rr = k * 16 + (tid >> 4);
+        for (int k = 0; k < kBlk * 16 / kColThreads; ++k) {
+            const int rr = k * (kColThreads / 16) + (tid >> 4);
             const int64_t r = r0 + rr;
             float v[8] = {};
             if (r < n) load8<T, WHOLE>(x + r * xs, c, d, v);
@@ -144,28 +145,31 @@ __global__ __launch_bounds__(256) void f8_columns_kernel(const T* x, int64_t n, 
                     const int64_t left = d - c;
                     if (left < 8) u = left <= 0 ? 0 : u & ((1ull << (8 * left)) - 1);
                     *reinterpret_cast<uint64_t*>(codes + r * kb * kBlk + c) = u;
-                    if ((lane & 15) == 0) scale[b * pitch + r] = (uint8_t)s.byte;
+                    if ((tid & 15) == 0) scale[b * pitch + r] = (uint8_t)s.byte;
                 }
             }
         }
         __syncthreads();
         const int cc = tid & 127, h = tid >> 7;
-        float v[64];
+        float v[kPart];
 #pragma unroll
-        for (int k = 0; k < 64; ++k) v[k] = to_f32(tile[h * 64 + k][cc]);
-        most[h][cc] = largest(v, 64);
+        for (int k = 0; k < kPart; ++k) v[k] = to_f32(tile[h * kPart + k][cc]);
+        most[h][cc] = largest(v, kPart);
         __syncthreads();
-        const BlockScale s = block_scale(fmaxf(most[0][cc], most[1][cc]), TYPE);
-        if (c0 + cc < d) {
-            uint8_t* const o = codes_t + (c0 + cc) * nb * kBlk + r0 + h * 64;
+        float m = most[0][cc];
 #pragma unroll
-            for (int k = 0; k < 64; k += 16) {
+        for (int k = 1; k < kParts; ++k) m = fmaxf(m, most[k][cc]);
+        const BlockScale s = block_scale(m, TYPE);
+        if (c0 + cc < d) {
+            uint8_t* const o = codes_t + (c0 + cc) * nb * kBlk + r0 + h * kPart;
+#pragma unroll
+            for (int k = 0; k < kPart; k += 16) {
                 v4i w;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     w[q] = codes4<TYPE>(v + k + q * 4, s);
                     if (s.bad) {  // zeros past the last row
-                        const int64_t left = n - (r0 + h * 64 + k + q * 4);
+                        const int64_t left = n - (r0 + h * kPart + k + q * 4);
                         if (left < 4) w[q] = left <= 0 ? 0 : w[q] & ((1 << (8 * (int)left)) - 1);
                     }
                 }
@@ -346,7 +350,7 @@ hipError_t launch_quantize(const T* x, int64_t n, int64_t d, int64_t xs, uint8_t
         const dim3 grid((uint32_t)(wgs < (1 << 20) ? wgs : 1 << 20));
         auto kernel = codes ? (whole ? f8_columns_kernel<T, TYPE, true, true> : f8_columns_kernel<T, TYPE, false, true>)
                             : (whole ? f8_columns_kernel<T, TYPE, true, false> : f8_columns_kernel<T, TYPE, false, false>);
-        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, x, n, d, xs, codes, scale, codes_t, scale_t);
+        hipLaunchKernelGGL(kernel, grid, dim3(kColThreads), 0, stream, x, n, d, xs, codes, scale, codes_t, scale_t);
     }
     return hipGetLastError();
 }
