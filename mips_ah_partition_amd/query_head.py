@@ -33,13 +33,14 @@ class QueryHead:
         trunk_type: "i8" (frozen) or "f8" (e4m3; `step` can train it)."""
         if trunk_type not in ("i8", "f8"):
             raise ValueError("trunk_type must be i8 or f8")
+        ahlib._act_code(act)
         if inner < 0 or not 0.0 <= drop < 1.0:
             raise ValueError("inner must not be negative, and drop in [0, 1)")
         self.trunk_type, self.inner, self.act, self.drop = trunk_type, int(inner), act, float(drop)
         if trunk_type == "i8":
             self.trunk8, self.trunk_scale = ahlib.ah_i8_quantize_rows(trunk)
         else:
-            self.trunk = trunk.float().clone()  # master copy
+            self.trunk = torch.clone(trunk.float(), memory_format=torch.contiguous_format)  # master copy
             self._codes = ahlib.ah_f8_quantize(self.trunk, want_columns=True)
         self.router = router.contiguous()
         L, k = router.shape

@@ -199,6 +199,6 @@ def test_no_rows_and_bad_arguments(gpu):
     head, items, hidden, ids, sc = _setup(torch, qh, 8, inner=40, drop=0.1, trunk_type="f8")
     loss, dx = head.step(hidden[:0], items, ids[:0], sc[:0], want_dx="hidden", trunk_lr=0.1)
     assert loss.shape == (0,) and dx.shape == (0, 96) and torch.isfinite(head.trunk).all()
-    for kw in (dict(trunk_type="f4"), dict(drop=1.0), dict(inner=-1)):
+    for kw in (dict(trunk_type="f4"), dict(drop=1.0), dict(inner=-1), dict(act="tanh")):
         with pytest.raises(ValueError):
             _setup(torch, qh, 8, **kw)

@@ -69,3 +69,38 @@ def test_gradient(gpu, m, L, d, n, p):  # noqa: F811
                            (dpre[:, n:], dh * f, e * (f.abs() + ef) * factor + dh.abs() * ef), (h, f * b * factor * some, ef * b.abs() * factor)):
         assert ((got.double() - want).abs() <= tol + (want.abs() + tol) * 2.0 ** -8).all()
     assert (dpre[flat < 0] == 0).all() and (h[flat < 0] == 0).all()
+
+
+STARTS = [(60, 64, 40), (60, 400, 40), (900, 128, 64), (900, 100, 30), (12096, 128, 512)]
+
+
+@pytest.mark.parametrize("m,k,n", STARTS)
+def test_rows_before_the_first_leaf(gpu, m, k, n):  # noqa: F811
+    """Rows before the first start and behind the last one belong to no leaf: zeros."""
+    torch, ah = gpu
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m + k)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, w, wo = rnd(m, k).bfloat16(), rnd(3, 2 * n, k).bfloat16(), rnd(3, k, n).bfloat16()
+    offsets = torch.tensor([5, m // 3, m // 3, m - 7], device="cuda")  # the second leaf's rows: none
+    h, pre = ah.ah_grouped_gated(x, w, offsets, want_pre=True)
+    d, hid = ah.ah_grouped_gated_grad(x, wo, pre, offsets)
+    for t in (h, pre, d, hid):
+        assert (t[:5] == 0).all() and (t[m - 7:] == 0).all() and torch.isfinite(t).all()
+    for a, b, l in ((5, m // 3, 0), (m // 3, m - 7, 2)):  # each leaf alone: other sizes, other orders of the sum
+        p = x[a:b].double() @ w[l].double().t()
+        e = (k + 16) * 2.0 ** -23 * (x[a:b].double().abs() @ w[l].double().abs().t())
+        assert ((pre[a:b].double() - p).abs() <= e + (p.abs() + e) * 2.0 ** -8).all()
+
+
+@pytest.mark.parametrize("m,k,n", STARTS)
+def test_starts_out_of_order(gpu, m, k, n):  # noqa: F811
+    """Starts have to ascend.  Others give rows of no meaning (leaves that overlap), and nothing outside the outputs."""
+    torch, ah = gpu
+    x, w, wo = (torch.ones(*s, device="cuda").bfloat16() for s in ((m, k), (3, 2 * n, k), (3, k, n)))
+    outs = [torch.full((m + 2, c), 7.0, device="cuda").bfloat16() for c in (n, 2 * n, 2 * n, n)]
+    offsets = torch.tensor([5, m // 2, m // 3, m - 7], device="cuda")
+    ah.ah_grouped_gated(x, w, offsets, out=outs[0][1:-1], pre_out=outs[1][1:-1])
+    ah.ah_grouped_gated_grad(x, wo, outs[1][1:-1], offsets, dpre_out=outs[2][1:-1], hidden_out=outs[3][1:-1])
+    for t in outs:
+        assert (t[0] == 7).all() and (t[-1] == 7).all()
