@@ -575,7 +575,8 @@ int ah_grouped_gated_grad(const void* dy, int64_t dy_stride, const void* w, int3
  *   x8, x_scale: m rows;  w8, w_scale: n rows;  k the summed length, the same for both;  bias float32 [n] or NULL;
  *   out [m][n]
  * ah_f8_linear: ah_f8_quantize of x, then ah_f8_matmul, the same results.
- *   workspace >= ah_f8_linear_workspace_bytes(m, k) bytes, 16-byte aligned
+ *   workspace >= ah_f8_linear_workspace_bytes(m, k) bytes, 16-byte aligned (0 up to 16 rows)
+ * Bytes of scale past n, up to np, are left as they are and not used.
  * Errors: AH_ERR_SHAPE (m, n < 0, k or d < 1, x_stride below the row), AH_ERR_UNSUPPORTED (a dtype, k or d >
  * AH_MAX_WIDTH, m or n > 2^30, n > AH_MAX_WIDTH with codes_t_out, a pointer not aligned), AH_ERR_NULL,
  * AH_ERR_WORKSPACE.  m == 0 or n == 0 is a successful no-op.

@@ -562,8 +562,9 @@ int ah_f8_linear(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t x
         return AH_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return AH_OK;
     if (!x || !w8 || !w_scale || !out) return AH_ERR_NULL;
-    if (!workspace || workspace_bytes < ah::f8_linear_workspace_bytes(m, k)) return AH_ERR_WORKSPACE;
-    if (!a16(workspace) || !a16(w8) || !a16(w_scale)) return AH_ERR_UNSUPPORTED;
+    const size_t need = ah::f8_linear_workspace_bytes(m, k);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return AH_ERR_WORKSPACE;
+    if ((need > 0 && !a16(workspace)) || !a16(w8) || !a16(w_scale)) return AH_ERR_UNSUPPORTED;
     const ah::F8Problem g{nullptr, nullptr, w8, w_scale, x_type, w_type, m, n, k};
     return hip_status(ah::launch_f8_linear(x, x_dtype, x_stride, g, bias, out, out_dtype, workspace,
                                            static_cast<hipStream_t>(stream)));

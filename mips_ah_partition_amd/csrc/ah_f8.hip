@@ -196,7 +196,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int6
     const int g = lane >> 4, li = lane & 15;
     const int32_t steps = (int32_t)(a.red / kBlk), s0 = (int32_t)((int64_t)steps * wave / kRowWaves),
                   s1 = (int32_t)((int64_t)steps * (wave + 1) / kRowWaves);
-    const int64_t j0 = (int64_t)blockIdx.x * 16, j = j0 + g * 4, p0 = (int64_t)blockIdx.y * 16 * FR;
+    const int64_t j0 = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * 16, j = j0 + g * 4, p0 = (int64_t)blockIdx.y * 16 * FR;
+    if (j0 >= a.J) return;
     const int64_t col = j0 + li < a.J ? j0 + li : a.J - 1;
     const char* const prow = a.p + col * a.ps + g * 16;
     const char* const psc = a.psc + col;
@@ -323,14 +324,16 @@ ProdArgs f8_args(const F8Problem& g, const float* bias, void* out, int32_t out_d
 
 template <int XT, int WT, int FR, int XB>
 hipError_t launch_few(const ProdArgs& a, int64_t k, bool whole, hipStream_t stream) {
-    const dim3 grid((uint32_t)((a.J + 15) / 16), (uint32_t)((a.T + 16 * FR - 1) / (16 * FR)));
+    const int64_t strips = (a.J + 15) / 16, most = kMaxGridItems / (kRowWaves * 64);  // of one launch dimension
+    const int64_t z = (strips + most - 1) / most;
+    const dim3 grid((uint32_t)((strips + z - 1) / z), (uint32_t)((a.T + 16 * FR - 1) / (16 * FR)), (uint32_t)z);
     hipLaunchKernelGGL((f8_few_kernel<XT, WT, FR, XB>), grid, dim3(kRowWaves * 64), 0, stream, a, k, whole);
     return hipGetLastError();
 }
 
 template <int XT, int WT>
 hipError_t launch_types(const ProdArgs& a, int64_t k, hipStream_t stream) {
-    if (rows_launchable(a.J) && a.T <= 64) {
+    if (a.T <= 64) {
         if (a.T <= 16) return launch_few<XT, WT, 1, 0>(a, k, true, stream);
         if (a.T <= 32) return launch_few<XT, WT, 2, 0>(a, k, true, stream);
         return launch_few<XT, WT, 4, 0>(a, k, true, stream);
@@ -383,16 +386,17 @@ hipError_t launch_f8_matmul(const F8Problem& g, const float* bias, void* out, in
     return launch_f8(g, f8_args(g, bias, out, out_dtype), stream);
 }
 
-// Workspace: the rows' codes, then their scale bytes.
+// Workspace: the rows' codes, then their scale bytes; none for rows that the product turns to codes itself.
+constexpr int64_t kFewRows = 16;
 static size_t f8_code_bytes(int64_t m, int64_t k) { return (size_t)m * ((k + kBlk - 1) / kBlk * kBlk); }
 size_t f8_linear_workspace_bytes(int64_t m, int64_t k) {
-    return f8_code_bytes(m, k) + (size_t)((k + kBlk - 1) / kBlk) * ((m + 15) / 16 * 16);
+    return m <= kFewRows ? 0 : f8_code_bytes(m, k) + (size_t)((k + kBlk - 1) / kBlk) * ((m + 15) / 16 * 16);
 }
 
 hipError_t launch_f8_linear(const void* x, int32_t dtype, int64_t xs, const F8Problem& p, const float* bias, void* out,
                             int32_t out_dtype, void* work, hipStream_t stream) {
     const int64_t bytes = dtype == AH_F32 ? 4 : 2;
-    if (p.m <= 16 && rows_launchable(p.n)) {
+    if (p.m <= kFewRows) {
         const bool whole = chunked(x, xs * bytes, 0) && p.k % 16 == 0;
         ProdArgs a = f8_args(p, bias, out, out_dtype);
         a.q = static_cast<const char*>(x);

@@ -1696,7 +1696,7 @@ int f8_shape(const ProdArgs& a) {
     const struct {
         int nq, np, per_cu;
         double rate;
-    } shapes[] = {{4, 4, 1, 1.0}, {3, 4, 1, 0.97}, {4, 3, 1, 0.97}, {2, 3, 1, 0.9}, {2, 2, 2, 0.85}};
+    } shapes[] = {{4, 4, 1, 1.0}, {3, 4, 1, 0.97}, {4, 3, 1, 0.97}, {2, 3, 1, 0.9}, {2, 2, 2, 0.85}, {1, 1, 2, 0.5}};
     int best = 0;
     double least = 0.0;
     for (const auto& s : shapes) {
@@ -1770,6 +1770,17 @@ hipError_t launch_rows(const ProdArgs& a, bool whole, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Gated products without FAST loads: 2 x 2 tiles, or, where those leave half the chip without one, 1 x 1 (gate: 1 x 2, of 64
+// columns), whose workgroups go through a quarter (half) of the epilogue each (1,500 rows of 21 leaves, 77 -> 200: gradient 16.0 us
+// -> 8.9, 77 -> 2 x 200 10.8 -> 8.5; 1,000 rows, 768 -> 2048: gradient 23 -> 17).
+template <int MODE, int DMA>
+hipError_t launch_small(const ProdArgs& a, hipStream_t stream) {
+    const int64_t J = MODE == kGate ? 2 * a.J : a.J;
+    if (row_tiles<MODE>(a, 128, false) * ((J + 127) / 128) <= kCUs)
+        return launch_tiles<MODE, 1, MODE == kGate ? 2 : 1, DMA>(a, stream);
+    return launch_tiles<MODE, 2, 2, DMA>(a, stream);
+}
+
 template <int MODE>
 hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     const int e = elem_bytes(MODE);
@@ -1796,7 +1807,9 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
             case 4: return launch_rows<MODE, 4>(a, whole, stream);
         }
     }
-    if constexpr (!is_f8(MODE)) {
+    if constexpr (is_gated(MODE)) {
+        if (!whole) return launch_small<MODE, 0>(a, stream);
+    } else if constexpr (!is_f8(MODE)) {
         if (!whole) return launch_tiles<MODE, 2, 2, 0>(a, stream);
     }
     if constexpr (MODE == kDw) {
@@ -1804,14 +1817,14 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     } else if constexpr (is_gated(MODE)) {
         // Other sums (and more than 4 GB of rows) take the general loads, at the smallest tile.
         if (a.red % 64 != 0 || a.red < 128 || a.T / fan * a.qs >= ((int64_t)1 << 32))
-            return launch_tiles<MODE, 2, 2, 1>(a, stream);
+            return launch_small<MODE, 1>(a, stream);
         switch (tile_shape<MODE>(a)) {
             case 4:
                 if constexpr (MODE == kGate) {  // float32 results would spill registers at 4 x 4
                     if (!a.out_f32) return launch_tiles<MODE, 4, 4, 2>(a, stream);
                 }
             case 3: return launch_tiles<MODE, 3, 4, 2>(a, stream);
-            default: return launch_tiles<MODE, 2, 2, 1>(a, stream);  // (with the ring's barriers 12 % slower)
+            default: return launch_small<MODE, 1>(a, stream);  // (with the ring's barriers 12 % slower)
         }
     } else if constexpr (is_f8(MODE)) {
         switch (f8_shape<MODE>(a)) {
@@ -1819,6 +1832,7 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
             case 34: return launch_tiles<MODE, 3, 4, 1>(a, stream);
             case 43: return launch_tiles<MODE, 4, 3, 1>(a, stream);
             case 23: return launch_tiles<MODE, 2, 3, 1>(a, stream);
+            case 11: return launch_tiles<MODE, 1, 1, 1>(a, stream);
             default: return launch_tiles<MODE, 2, 2, 1>(a, stream);
         }
     } else {

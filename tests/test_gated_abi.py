@@ -75,7 +75,7 @@ def test_f8_matmul(lib, kw, want):
     assert lib.ah_f8_matmul(*_with(MATMUL, **kw)) == want
 
 
-LINEAR = dict(x=F, dt=1, m=2, k=16, xs=16, xt=0, w8=F, ws=F, wt=0, n=5, bias=None, out=F, odt=1, work=F, bytes=BIG,
+LINEAR = dict(x=F, dt=1, m=20, k=16, xs=16, xt=0, w8=F, ws=F, wt=0, n=5, bias=None, out=F, odt=1, work=F, bytes=BIG,
               stream=None)
 
 
@@ -83,9 +83,10 @@ LINEAR = dict(x=F, dt=1, m=2, k=16, xs=16, xt=0, w8=F, ws=F, wt=0, n=5, bias=Non
     (dict(m=-1), SHAPE), (dict(xs=15), SHAPE), (dict(dt=7), UNSUPPORTED), (dict(xt=3), UNSUPPORTED),
     (dict(wt=3), UNSUPPORTED), (dict(odt=-1), UNSUPPORTED), (dict(k=(1 << 20) + 1, xs=1 << 21), UNSUPPORTED),
     (dict(x=None), NULL), (dict(w8=None), NULL), (dict(out=None), NULL), (dict(work=None), WORKSPACE),
-    (dict(bytes=271), WORKSPACE), (dict(work=ODD), UNSUPPORTED), (dict(w8=ODD), UNSUPPORTED), (dict(m=0, x=None), 0)])
+    (dict(bytes=2591), WORKSPACE), (dict(work=ODD), UNSUPPORTED), (dict(w8=ODD), UNSUPPORTED), (dict(m=0, x=None), 0)])
 def test_f8_linear(lib, kw, want):
-    assert lib.ah_f8_linear_workspace_bytes(2, 16) == 272  # two rows of 128 codes, 16 scale bytes
+    assert lib.ah_f8_linear_workspace_bytes(20, 16) == 2592  # rows of 128 codes, 32 scale bytes
+    assert lib.ah_f8_linear_workspace_bytes(16, 16) == 0  # few rows need none
     assert lib.ah_f8_linear(*_with(LINEAR, **kw)) == want
 
 
