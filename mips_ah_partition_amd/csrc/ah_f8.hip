@@ -81,7 +81,8 @@ __device__ __forceinline__ float largest(const float* v, int n) {  // +inf where
     return bad ? INFINITY : m;
 }
 
-// Rows to codes.  16 lanes have a block of 128, 8 elements each; a wave four blocks of a row.
+// Rows to codes.  HBM-bound (2 or 4 bytes in, 1 out; bfloat16 8192 x 4096: 24 us, 4.2 TB/s).  16 lanes have a block of
+// 128, 8 elements each (one or two loads of 16 bytes and a store of 8), a wave four blocks of a row: no barrier, no LDS.
 template <typename T, int TYPE, bool WHOLE>
 __global__ __launch_bounds__(256) void f8_rows_kernel(const T* x, int64_t n, int64_t d, int64_t xs, uint8_t* codes,
                                                       uint8_t* scale) {
@@ -107,7 +108,9 @@ __global__ __launch_bounds__(256) void f8_rows_kernel(const T* x, int64_t n, int
 }
 
 // Columns to codes (the transposed matrix), and rows too where wanted, from one reading: a workgroup has 128 x 128
-// elements, its rows' blocks in registers, its columns' through LDS, 32 elements of a column a thread.
+// elements, its rows' blocks in registers, its columns' through LDS, 32 elements of a column a thread.  Bfloat16 8192 x
+// 4096 to both: 33-36 us (134 MB, 4.0 TB/s; two passes would read 67 MB more), 8192 x 1536 to columns 11.6; 256 threads, 64
+// elements of a column each: 36, and 500 x 77 9.1 instead of 6.1.  Bound by the memory and the two barriers a tile.
 constexpr int kColThreads = 512, kParts = kColThreads / kBlk, kPart = kBlk / kParts;
 template <typename T, int TYPE, bool WHOLE, bool ROWS>
 __global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int64_t n, int64_t d, int64_t xs, uint8_t* codes,
@@ -185,7 +188,8 @@ __global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int
 // of 128, load both operands from memory into the matrix instruction's layout (lane 16 g + i: bytes 16 g .. and 64 + 16 g ..
 // of row i) and add up through LDS in a fixed order.  XB = 2 or 4: the rows are of that many bytes an element, and every
 // workgroup turns them to codes for itself (a block's largest value lies in four lanes of the wave that needs it, so
-// nothing waits): one launch instead of two.  Up to 16 rows: of 37 x 1001 it took 12.4 us on the GPU, quantising and
+// nothing waits): one launch instead of two.  One row, 1536 -> 4096: 6.0-6.5 us on the GPU, a launch and the chain of
+// loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a launch to quantise.  Up to 16 rows: of 37 x 1001 it took 12.4 us on the GPU, quantising and
 // product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are aligned and 16 elements inside the row or outside together.
 template <int XT, int WT, int FR, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int64_t k, bool whole) {

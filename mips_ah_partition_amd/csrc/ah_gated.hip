@@ -1,5 +1,6 @@
 // Gated feed-forward by leaf: the products of ah_tiles.hpp whose epilogues activate, multiply and drop, and, back, turn
-// the hidden values' gradient into the two projections'.
+// the hidden values' gradient into the two projections'.  Neither the projections' sums nor the hidden values' gradient (of
+// 16,384 rows and 4,096 columns 0.5 and 0.27 GB in float32) leave the registers they are made in.
 #include "ah_tiles.hpp"
 
 namespace ah {

@@ -455,6 +455,10 @@ __device__ __forceinline__ void take_row(v4f (&acc)[FQ][FP], int x, v4f (&t)[FP]
         }
 }
 
+// Gated product, 16,384 rows of 16 leaves, 1536 -> 2 x 4096 (412 GFLOP), dropout, both projections kept: 541-575 us at 4 x 4.
+// The contraction takes 380 of them (without its loads 285; a dense library product of the size 380); what no matrix
+// instruction covers are the stores (402 MB, all CUs at once: 77, 5.2 TB/s), the activation and its rounding (73) and Philox
+// (46).  Matrix instructions run in 0.36 of the clocks, at 2.0 GHz.
 // A wave's part of a gated product: a lane holds gate and up of the same columns, in fragments NP apart.  The
 // activation is a template's, chosen once a tile: chosen for each element the compiler computes all and selects.  WHOLE:
 // all the tile's columns exist, so that nothing but the rows is asked about.
@@ -517,6 +521,10 @@ __device__ __forceinline__ void eight_columns(v4f f0, v4f f1, float* v) {
         v[4 + e] = __uint_as_float(t[1]);
     }
 }
+// Gated gradient, 16,384 rows of 16 leaves, 1536 -> 4096 (206 GFLOP, 922 MB), dropout, hidden values too: 370-390 us at 3 x 4,
+// the contraction 172 of them (without its loads 140), stores 80 (402 MB), the reads of the projections 35, Philox 27, the
+// rest is the activation, its derivative and their rounding: one after another on every CU, matrix instructions in 0.25 of
+// the clocks.  4 x 4 would not leave registers for a fragment row's projections on their way.
 // A wave's part of the gradient: dh becomes (da, db) and h.  The projections of fragment row x + 1 are asked for before
 // row x is dealt with; where the tile is WHOLE without a branch (rows that are not written read row 0), behind which the
 // compiler would wait for all of them.
@@ -660,6 +668,7 @@ __device__ __forceinline__ uint32_t query_of(const ProdArgs& a, uint32_t s) {
 // TFLOP/s; zeros 2.40 GHz), with the LDS reads of a step 1661; the int8 kernel runs at 1.9 GHz, the bfloat16
 // one at 1.4 to 1.6.  Without the loads, the barrier or the wait for them (8192 x 6144 x 4096, bfloat16) 360, 422
 // and 442 us instead of 446, on zeros 337.
+// The gated and 8-bit float products, and what bounds them, stand with their epilogues and half-steps.
 template <int MODE, int NQ, int NP, int OB, int DMA>
 __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(ProdArgs a) {
     constexpr int ELEM = elem_bytes(MODE), FQ = 2 * NQ, FP = 2 * NP, NB = NQ + NP;
@@ -1023,8 +1032,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     };
     // FAST.  LDS is a ring of four half-steps (64 bytes of the sum: 4 KB a block).  Half-step h is multiplied from registers
     // while h + 1 is read from the ring and the loads of h + 4 go where h was, so that a load has two to three half-steps to
-    // arrive, where two buffers of whole steps give it one to two (the wait for them was a third of the loop: 410 us of
-    // 16,384 rows x 1536 -> 2 x 4096 without a store, 265 without the loads).  One read or one load stands between two
+    // arrive, where two buffers of whole steps give it one to two (16,384 rows, 1536 -> 2 x 4096, without stores: 410 us with two
+    // buffers, 380 with the ring, 285 without the loads).  One read or one load stands between two
     // matrix instructions; column fragments are read first, since the next half's first FP instructions use all of them.
     constexpr uint32_t SLOT = NB * 4096;
     const uint32_t qring = base + NP * 4096 + (wq * 32 * NQ + li) * 64 + ((g ^ turn4(li >> 2)) * 16);
@@ -1080,8 +1089,9 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // float8: half-step kk multiplies half of the row fragments with all column fragments; the first reads the other half,
     // the second, once a column fragment is done with, the next step's, and the first row fragments.  Between two matrix
     // instructions (32 clocks) stands one load or one fragment's reads: in a lump behind every fourth they cost the
-    // pipe (8192 x 4096 x 16384: 627 us with them).  So that a load is three instructions its address is a uniform one
-    // and a lane's offset, the same all along a tile.
+    // pipe (8192 x 4096 x 16384, quantising included: 627 us, spread 547).  So that a load is three instructions its address is a uniform one
+    // and a lane's offset, the same all along a tile.  That product alone takes 445-515 us (2.1-2.5 PFLOP/s), matrix
+    // instructions in 0.54 of the clocks at 1.9-2.0 GHz; without the stores, or without the loads, 60 less.
     auto load8_chunk = [&](int u, int c, uint32_t buf) {
         if constexpr (F8) {
             const bool in = u * STEP < w.red;
@@ -1111,7 +1121,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
         }
         // The second half-step does not use the first's sums: without a use of them here the compiler moves the first's
-        // matrix instructions behind the barrier too, whose wait then nothing covers (554 us).
+        // matrix instructions behind the barrier too, whose wait then nothing covers (554 us instead of 513).
         if (kk == 0) {
 #pragma unroll
             for (int n = 0; n < H; ++n)
@@ -1434,7 +1444,9 @@ __device__ __forceinline__ float step_of(float m) { return m < INFINITY ? m / 12
 // latency (7.0 on the GPU; 15.6 with tiles and quantising in a launch of its own).
 constexpr int kRowWaves = 8;
 // STRIP (gated sums of at most 512 bytes, eight pieces): nothing to share out, so every wave has 16 columns of its own and the
-// whole sum (999 slots of 37 leaves, 100 -> 2 x 385: 18 us with the sum shared by eight waves).
+// whole sum (999 slots of 37 leaves, 100 -> 2 x 385, on the GPU: 12.4 us, 18 with the sum shared by eight waves).  Bound
+// by the chain of leaf starts, order, row and weights, each a load that waits for the one before.  One token, 1536 ->
+// 2 x 4096, shares the sum: 7.5 us, of which 25 MB of weights are 4.7.
 template <int MODE, int FR, bool WHOLE, int XB, bool STRIP = false>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
     constexpr int ELEM = elem_bytes(MODE), U = STRIP ? 2 : 4, G = MODE == kGate ? 2 : 1;
@@ -1681,34 +1693,70 @@ int64_t row_tiles(const ProdArgs& a, int64_t TQ, bool most) {
 template <int MODE>
 int tile_shape(const ProdArgs& a) {
     auto time = [&](int64_t TQ, int64_t TP, int64_t resident, double round) {
-        const int64_t J = MODE == kGate ? 2 * a.J : a.J;
-        return (double)((row_tiles<MODE>(a, TQ, false) * ((J + TP - 1) / TP) + resident - 1) / resident) * round;
+        return (double)((row_tiles<MODE>(a, TQ, false) * ((a.J + TP - 1) / TP) + resident - 1) / resident) * round;
     };
-    const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / (MODE == kGate ? 0.87 : 0.97)),
+    const double t4 = time(256, 256, kCUs, 16), t3 = time(192, 256, kCUs, 12 / 0.97),
                  t2 = time(128, 128, 2 * kCUs, 8 / 0.85);
     return t2 <= t3 && t2 <= t4 ? 2 : t3 < t4 ? 3 : 4;
 }
 
-// The same for float8, whose gradients have few tiles and long sums, so that the shape that fills the chip's
-// rounds best wins: 10 NQ + NP.  Rates relative to 4 x 4 on large products.
-template <int MODE>
-int f8_shape(const ProdArgs& a) {
-    const struct {
-        int nq, np, per_cu;
-        double rate;
-    } shapes[] = {{4, 4, 1, 1.0}, {3, 4, 1, 0.97}, {4, 3, 1, 0.97}, {2, 3, 1, 0.9}, {2, 2, 2, 0.85}, {1, 1, 2, 0.5}};
+// The same for gated and 8-bit float products, whose tiles end in epilogues of their own weight and whose sums may be long
+// over few tiles: a round of the resident workgroups takes (steps of its sum) x step + end, and, with two workgroups a CU, a
+// last round of one a CU the share `alone` of that.  Measured, us:
+//   8-bit float           4 x 4   3 x 4   4 x 3   2 x 3   2 x 2   1 x 1
+//   8192 x 4096 x 16384     461     501     509     637     544    1248
+//   8192 x 4096 x 1536       52      82      46      59      57     119
+//   1536 x 8192 x 4096       90      74      74     105      60     113
+//   4096 x 8192 x 1536       92      76      75      57      60     115
+//   16384 x 1024 x 2048      48      49      49      57      44      91
+//   2048 x 4096 x 1536       50      41      41      31      27      39
+//   333 x 4096 x 1001        52      42      43      29      23      17
+//   gate, rows of 16 leaves                4 x 4   3 x 4   2 x 2      gradient   3 x 4   2 x 2
+//   16384, 1536 -> 2 x 4096                  553     609     645                   386     439
+//   16384, 768 -> 2 x 1024                   107      91      79                    79      69
+//   4096, 1536 -> 2 x 2048                   115     101      84                    59      68
+// The figures below are fits to these and to more sizes.
+struct TileCost {
+    int nq, np, per_cu;
+    double step, end, alone;  // us, us, share
+};
+template <int MODE, int N>
+int cheapest(const ProdArgs& a, const TileCost (&shapes)[N], int64_t J, int64_t steps) {
     int best = 0;
     double least = 0.0;
     for (const auto& s : shapes) {
-        const int64_t tiles = row_tiles<MODE>(a, s.nq * 64, false) * ((a.J + s.np * 64 - 1) / (s.np * 64)),
-                      resident = kCUs * s.per_cu;
-        const double time = (double)((tiles + resident - 1) / resident) * s.nq * s.np * s.per_cu / s.rate;
+        const int64_t TQ = s.nq * 64, TP = s.np * 64;
+        // every second leaf ends inside a tile of its own
+        const int64_t ends = is_plain(MODE) ? 0 : (a.T < a.L ? a.T : a.L) / 2;
+        const int64_t tiles = ((a.T + TQ - 1) / TQ + ends) * ((J + TP - 1) / TP);
+        const int64_t resident = (int64_t)kCUs * s.per_cu, rest = tiles % resident;
+        const double rounds = (double)(tiles / resident) + (rest == 0 ? 0.0 : rest <= kCUs ? s.alone : 1.0);
+        const double time = rounds * ((double)steps * s.step + s.end);
         if (best == 0 || time < least) {
             best = s.nq * 10 + s.np;
             least = time;
         }
     }
     return best;
+}
+template <int MODE>
+int f8_shape(const ProdArgs& a) {
+    const TileCost shapes[] = {{4, 4, 1, 1.45, 11.0, 1.0}, {3, 4, 1, 1.21, 6.7, 1.0}, {4, 3, 1, 1.21, 6.7, 1.0},
+                               {2, 3, 1, 0.84, 3.0, 1.0},  {2, 2, 2, 0.96, 3.3, 0.7},  {1, 1, 2, 0.57, 1.1, 1.0}};
+    return cheapest<MODE>(a, shapes, a.J, (a.red + 127) / 128);
+}
+template <int MODE>
+int gated_shape(const ProdArgs& a) {
+    const int64_t steps = (a.red + 63) / 64;
+    if constexpr (MODE == kGate) {
+        const TileCost f32[] = {{3, 4, 1, 1.65, 10.5, 1.0}, {2, 2, 2, 1.32, 4.0, 0.5}};  // (4 x 4 would spill registers)
+        if (a.out_f32) return cheapest<MODE>(a, f32, 2 * a.J, steps);
+        const TileCost shapes[] = {f32[0], f32[1], {4, 4, 1, 2.1, 10.0, 1.0}};
+        return cheapest<MODE>(a, shapes, 2 * a.J, steps);
+    } else {
+        const TileCost shapes[] = {{3, 4, 1, 2.0, 14.5, 1.0}, {2, 2, 2, 1.55, 12.5, 0.45}};
+        return cheapest<MODE>(a, shapes, a.J, steps);
+    }
 }
 
 template <int MODE, int NQ, int NP, int DMA>
@@ -1818,12 +1866,10 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
         // Other sums (and more than 4 GB of rows) take the general loads, at the smallest tile.
         if (a.red % 64 != 0 || a.red < 128 || a.T / fan * a.qs >= ((int64_t)1 << 32))
             return launch_small<MODE, 1>(a, stream);
-        switch (tile_shape<MODE>(a)) {
-            case 4:
-                if constexpr (MODE == kGate) {  // float32 results would spill registers at 4 x 4
-                    if (!a.out_f32) return launch_tiles<MODE, 4, 4, 2>(a, stream);
-                }
-            case 3: return launch_tiles<MODE, 3, 4, 2>(a, stream);
+        switch (gated_shape<MODE>(a)) {
+            case 44:
+                if constexpr (MODE == kGate) return launch_tiles<MODE, 4, 4, 2>(a, stream);
+            case 34: return launch_tiles<MODE, 3, 4, 2>(a, stream);
             default: return launch_small<MODE, 1>(a, stream);  // (with the ring's barriers 12 % slower)
         }
     } else if constexpr (is_f8(MODE)) {

@@ -9,7 +9,8 @@ pytestmark = pytest.mark.gpu
 
 # m, k, n: 256 x 256, 192 x 256, 256 x 192, 128 x 192 and 128 x 128 tiles; one step of the sum (k <= 128), two, three and more; ragged ends
 CASES = [(8192, 256, 2048), (8192, 100, 2048), (8192, 1000, 2000), (8064, 256, 1536), (8000, 60, 1530), (8192, 512, 1536), (8190, 128, 1500),
-         (4096, 384, 1536), (4001, 700, 1531), (4096, 256, 1536), (900, 120, 900)]
+         (4096, 384, 1536), (4001, 700, 1531), (4096, 256, 1536), (900, 120, 900),
+         (8200, 2048, 1500), (4000, 1300, 4000), (5400, 300, 1500), (8100, 300, 1500)]
 
 
 @pytest.mark.parametrize("out", ["bfloat16", "float32"])

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 # m, L, k, n: one leaf and several with ragged ends, 2 to 32 steps of 64, whole and partial columns
 CASES = [(16128, 1, 128, 512), (12096, 1, 128, 512), (15000, 3, 192, 500), (11300, 4, 320, 520), (12096, 1, 2048, 512), (16128, 1, 1600, 512),
-         (40000, 5, 256, 136)]
+         (40000, 5, 256, 136), (22000, 3, 1024, 136), (12096, 1, 1024, 512), (30000, 5, 1600, 132)]
 
 
 @pytest.mark.parametrize("p", [0.0, 0.25])
