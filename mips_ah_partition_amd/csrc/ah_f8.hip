@@ -189,8 +189,8 @@ __global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int
 // of row i) and add up through LDS in a fixed order.  XB = 2 or 4: the rows are of that many bytes an element, and every
 // workgroup turns them to codes for itself (a block's largest value lies in four lanes of the wave that needs it, so
 // nothing waits): one launch instead of two.  One row, 1536 -> 4096: 6.0-6.5 us on the GPU, a launch and the chain of
-// loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a launch to quantise.  Up to 16 rows: of 37 x 1001 it took 12.4 us on the GPU, quantising and
-// product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are aligned and 16 elements inside the row or outside together.
+// loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a launch to quantise.  Up to 16 rows: of
+// 37 x 1001 it took 12.4 us on the GPU, quantising and product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are aligned and 16 elements inside the row or outside together.
 template <int XT, int WT, int FR, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int64_t k, bool whole) {
     constexpr int U = FR == 4 ? 2 : 4, MODE = kF8 + XT + 2 * WT;
@@ -335,14 +335,45 @@ hipError_t launch_few(const ProdArgs& a, int64_t k, bool whole, hipStream_t stre
     return hipGetLastError();
 }
 
+// Row fragments of f8_few_kernel, or 0 for tiles, which take `tiles` us (f8_shape): its time is a chain of loads and matrix
+// instructions for every eight steps and the start of its workgroups, or what they read, from L2 mostly, each 16 columns and
+// 16 FR rows.  Few columns and long sums are its own, however many the rows; many columns of more than 16 rows are the
+// tiles'.  Measured, us, FR = 1, 2, 4 and the tiles:
+//   100 x 8192 x 100       9.6   13.5   20.7   28.0          64 x 4096 x 4096      17.7   15.2   12.8   15.7
+//   300 x 4096 x 300       9.8    8.3   12.0   16.2          64 x 4096 x 16384     61.2   53.6   45.2   16.7
+//   500 x 200 x 77         2.9    3.1    3.5    4.4          333 x 4096 x 1001     24.7   21.7   23.6   16.0
+//   256 x 768 x 384        3.9    3.8    4.6    5.9          1024 x 768 x 384       7.9    7.6    7.8    5.9
+int few_fragments(const ProdArgs& a, double tiles) {
+    if (a.T <= 16) return 1;  // as ah_f8_linear's product that quantises, whose sums are to be the same
+    const struct {
+        int fr;
+        double chain, starts, rate;  // us for every eight steps, workgroups a us beyond one a CU, MB a us
+    } few[] = {{1, 0.9, 420, 7.0}, {2, 1.4, 200, 5.5}, {4, 2.3, 60, 7.0}};
+    int best = 0;
+    for (const auto& f : few) {
+        const int64_t rows = (a.T + 16 * f.fr - 1) / (16 * f.fr), wgs = rows * ((a.J + 15) / 16), steps = (a.red + 127) / 128;
+        const double start = (double)((steps + kRowWaves - 1) / kRowWaves) * f.chain +
+                             (wgs > kCUs ? (double)(wgs - kCUs) / f.starts : 0.0),
+                     read = (double)wgs * 16 * (1 + f.fr) * (double)a.red * 1e-6 / f.rate, time = 2.0 + (start > read ? start : read);
+        if (rows <= 65535 && time < tiles) {  // (a launch's second dimension)
+            best = f.fr;
+            tiles = time;
+        }
+    }
+    return best;
+}
+
 template <int XT, int WT>
 hipError_t launch_types(const ProdArgs& a, int64_t k, hipStream_t stream) {
-    if (a.T <= 64) {
-        if (a.T <= 16) return launch_few<XT, WT, 1, 0>(a, k, true, stream);
-        if (a.T <= 32) return launch_few<XT, WT, 2, 0>(a, k, true, stream);
-        return launch_few<XT, WT, 4, 0>(a, k, true, stream);
+    constexpr int MODE = kF8 + XT + 2 * WT;
+    double tiles;
+    f8_shape<MODE>(a, &tiles);
+    switch (few_fragments(a, tiles + 2.0)) {  // (a launch)
+        case 1: return launch_few<XT, WT, 1, 0>(a, k, true, stream);
+        case 2: return launch_few<XT, WT, 2, 0>(a, k, true, stream);
+        case 4: return launch_few<XT, WT, 4, 0>(a, k, true, stream);
+        default: return launch_prod<MODE>(a, 1, stream);
     }
-    return launch_prod<kF8 + XT + 2 * WT>(a, 1, stream);
 }
 
 hipError_t launch_f8(const F8Problem& g, const ProdArgs& a, hipStream_t stream) {

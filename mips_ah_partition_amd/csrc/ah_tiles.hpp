@@ -676,13 +676,19 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     constexpr bool PERM = kPerm<MODE, OB>, GATE = MODE == kGate, F8 = is_f8(MODE), FAST = DMA == 2;
     constexpr int TQ = NQ * 64, TP = NP * 64 / (GATE ? 2 : 1), STEP = 128 / ELEM;
     constexpr int BUF = NB * kBlock;
+    // Steps in LDS at a time: two; float8 at 64 x 64, where a step's matrix instructions (128 clocks a wave) cover nothing of a
+    // load's way: four (DMA 3), so that a load has three steps to arrive (1000 x 8192 x 400: 38 us with two, 27 with four; up to
+    // eight steps two: 8192 x 128 x 100 4.5 us, with four 6.4).
+    constexpr int D = DMA == 3 ? 4 : 2, RING = D * BUF, LOADS = 2 * NB + (F8 ? 1 : 0);
+    static_assert(D == 2 || (F8 && NQ * NP == 1));
+    static_assert(!F8 || ((TQ > TP ? TQ : TP) * (D - 1) * STEP <= (int)sizeof(zero_rows)));
     // Rows that a thread loads of a row operand's 64, in how many loads: FAST one of 16 bytes of 64, else two of 128.
     constexpr int RH = FAST ? 64 : 32, QS = FAST ? NQ : 2 * NQ;
     constexpr int QR = QCOL ? 2 : PLAIN || FAST ? 1 : 2 * NQ, SLOTS = MODE == kDw ? 2 : QS;
-    __shared__ __align__(1024) char lds[(DMA ? 2 : 1) * BUF];
+    __shared__ __align__(1024) char lds[(DMA ? D : 1) * BUF];
     __shared__ __align__(16) char turns[OB == 4 && !GATE ? 4 * 16 * kTurnPitch<NP> : 16];
     __shared__ __align__(16) float scales[MODE == kI8 ? 128 * NP + 64 * NQ : F8 ? 64 * NP : 4];
-    __shared__ __align__(16) char sbytes[F8 ? 2 * kScaleBuf : 16];  // float8: a step's scale bytes, Q's 256 and P's
+    __shared__ __align__(16) char sbytes[F8 ? D * kScaleBuf : 16];  // float8: a step's scale bytes, Q's 256 and P's
     __shared__ LocateShared sh;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wq = wave >> 1, wp = wave & 1, g = lane >> 4, li = lane & 15;
@@ -726,7 +732,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     const bool spread = MODE == kDw && each >= 8;
     const int64_t per = spread ? eighth * a.L : (total + 7) >> 3;
     const int64_t tbeg = (int64_t)(blockIdx.x & 7) * per, tend = spread || tbeg + per < total ? tbeg + per : total;
-    auto steps = [&](int32_t red) { return red <= 2 * STEP ? 2 : (red + STEP - 1) / STEP; };
+    auto steps = [&](int32_t red) { return red <= D * STEP ? D : (red + STEP - 1) / STEP; };
     // Publishes tile t in sh.next[k] (to be read after a barrier); past the last one, rows of nothing.
     auto find = [&](int64_t t, int k) {
         int32_t tq, tp;
@@ -1101,7 +1107,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     };
     auto half_step8 = [&](int kk, uint32_t buf, int u) {
         constexpr int H = FQ / 2;
-        const int b = buf ? 1 : 0;
+        const int b = D == 2 ? (buf ? 1 : 0) : (int)(buf / BUF), bl = D == 2 ? 1 - b : (b + D - 1) % D;  // read, loaded
+        const uint32_t to = D == 2 ? BUF - buf : (buf + RING - BUF) % RING;
 #pragma unroll
         for (int y = 0; y < FP; ++y) {
 #pragma unroll
@@ -1112,8 +1119,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
                     constexpr int S = FP * H;  // evenly: the four waves' 1 KB take the address unit 16 clocks each
 #pragma unroll
                     for (int c = 0; c < 2 * NB; ++c)
-                        if (c * S / (2 * NB) == at) load8_chunk(u, c, BUF - buf);
-                    if (at == S - 2) load_scale_bytes(u, 1 - b);
+                        if (c * S / (2 * NB) == at) load8_chunk(u, c, to);
+                    if (at == S - 2) load_scale_bytes(u, bl);
                     if (x == H - 1) read_p8(y, b);
                 }
                 if (x == 0 && y < H) read_q8(kk ^ 1, y, b);
@@ -1179,6 +1186,13 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         if (tid < 64 * NQ) scales[128 * NP + tid] = v[2];
     };
 
+    // The same straight to LDS (every wave the same): with the values in a register on their way the compiler would wait for
+    // it, and so for every load, in each step.  Three steps of at least four follow before they are read.
+    auto load_bias = [&](const Tile& n) {
+        const int64_t j = n.j0 + lane < a.J ? n.j0 + lane : a.J - 1;
+        dma4(a.bias ? reinterpret_cast<const char*>(a.bias + j) : reinterpret_cast<const char*>(zero_rows), lds_addr(scales));
+    };
+
     const uint64_t call_step = is_gated(MODE) && a.drop.t ? step_of_call(a.drop) : 0;
     auto store = [&](const int32_t(&rows)[2], const Tile& n) {
         if constexpr (is_gated(MODE)) {
@@ -1237,7 +1251,7 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
         for (int u = 0; u < 2; ++u) rows_l[u] = rows_s[u];
         set_addresses();
 #pragma unroll
-        for (; ul < 2; ++ul) {
+        for (; ul < D; ++ul) {
             if constexpr (MODE == kDw) {
                 if (ul == 0)
                     set_rows(0, slot);
@@ -1255,14 +1269,14 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             }
             load_scale_bytes(ul, ul);
         }
-        us = 1;
+        us = D - 1;
         advance_order();
         Tile wc = w;  // what is multiplied
         int32_t uc = 0, rows_c[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) rows_c[u] = rows_l[u];
         clear();
-        land<FAST ? 3 * NB : 2 * NB>();  // (float8: a wave has up to one more of step 1 in flight)
+        land<FAST ? 3 * NB : (D - 1) * LOADS>();
         if constexpr (FAST) {
 #pragma unroll
             for (int x = 0; x < FQ; ++x) qf[0][x] = ring_q(x, 0);
@@ -1279,22 +1293,28 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
 #pragma unroll
             for (int x = 0; x < FP; ++x) pf[0][x] = read_p(x, 0, 0);
         }
-        for (uint32_t cur = 0;; cur = BUF - cur) {
+        for (uint32_t cur = 0, next;; cur = next) {
+            next = D == 2 ? BUF - cur : (cur + BUF) % RING;
             float sv[3] = {};
             if constexpr (PLAIN) {
-                if (uc == 0) load_scales(wc, sv);
+                if (uc == 0 && D == 2) load_scales(wc, sv);
             }
             if constexpr (FAST) {
                 land<2 * NB>();  // half-step 1 of this step is there; two are in flight
             } else if constexpr (F8) {
                 half_step8(0, cur, 0);
-                land<0>();
+                land<(D - 2) * LOADS>();
             } else {
                 half_step(0, cur, 0);
                 land<0>();
             }
             if constexpr (PLAIN) {
-                if (uc == 0) keep_scales(sv);
+                if (uc == 0) {
+                    if constexpr (D > 2)
+                        load_bias(wc);
+                    else
+                        keep_scales(sv);
+                }
             }
             if (ul == w.nt) {
                 w = ws;
@@ -1306,13 +1326,13 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
             if constexpr (MODE == kDw) set_rows(ul, slot);
             advance_order();
             if constexpr (F8) {
-                half_step8(1, BUF - cur, ul++);
+                half_step8(1, next, ul++);
             } else if constexpr (FAST) {  // cur: the half-steps of this step, in LDS at cur and cur + SLOT
                 half_ring(0, cur + SLOT, cur, ul);
                 land<2 * NB>();
-                half_ring(1, BUF - cur, cur + SLOT, ul++);
+                half_ring(1, next, cur + SLOT, ul++);
             } else {
-                half_step(1, BUF - cur, ul++);
+                half_step(1, next, ul++);
             }
             if (++uc < wc.nt) continue;
             if constexpr (NQ * NP > 4 || is_gated(MODE)) settle();
@@ -1721,7 +1741,7 @@ struct TileCost {
     double step, end, alone;  // us, us, share
 };
 template <int MODE, int N>
-int cheapest(const ProdArgs& a, const TileCost (&shapes)[N], int64_t J, int64_t steps) {
+int cheapest(const ProdArgs& a, const TileCost (&shapes)[N], int64_t J, int64_t steps, double* least_time = nullptr) {
     int best = 0;
     double least = 0.0;
     for (const auto& s : shapes) {
@@ -1737,13 +1757,14 @@ int cheapest(const ProdArgs& a, const TileCost (&shapes)[N], int64_t J, int64_t 
             least = time;
         }
     }
+    if (least_time) *least_time = least;
     return best;
 }
 template <int MODE>
-int f8_shape(const ProdArgs& a) {
+int f8_shape(const ProdArgs& a, double* time = nullptr) {
     const TileCost shapes[] = {{4, 4, 1, 1.45, 11.0, 1.0}, {3, 4, 1, 1.21, 6.7, 1.0}, {4, 3, 1, 1.21, 6.7, 1.0},
-                               {2, 3, 1, 0.84, 3.0, 1.0},  {2, 2, 2, 0.96, 3.3, 0.7},  {1, 1, 2, 0.57, 1.1, 1.0}};
-    return cheapest<MODE>(a, shapes, a.J, (a.red + 127) / 128);
+                               {2, 3, 1, 0.84, 3.0, 1.0},  {2, 2, 2, 0.96, 3.3, 0.7},  {1, 1, 2, 0.57, 3.0, 0.65}};
+    return cheapest<MODE>(a, shapes, a.J, (a.red + 127) / 128, time);
 }
 template <int MODE>
 int gated_shape(const ProdArgs& a) {
@@ -1878,7 +1899,7 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
             case 34: return launch_tiles<MODE, 3, 4, 1>(a, stream);
             case 43: return launch_tiles<MODE, 4, 3, 1>(a, stream);
             case 23: return launch_tiles<MODE, 2, 3, 1>(a, stream);
-            case 11: return launch_tiles<MODE, 1, 1, 1>(a, stream);
+            case 11: return a.red > 8 * 128 ? launch_tiles<MODE, 1, 1, 3>(a, stream) : launch_tiles<MODE, 1, 1, 1>(a, stream);
             default: return launch_tiles<MODE, 2, 2, 1>(a, stream);
         }
     } else {

@@ -7,10 +7,13 @@ from test_gpu_f8 import _values, gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-# m, k, n: 256 x 256, 192 x 256, 256 x 192, 128 x 192 and 128 x 128 tiles; one step of the sum (k <= 128), two, three and more; ragged ends
+# m, k, n: 256 x 256, 192 x 256, 256 x 192, 128 x 192, 128 x 128 and 64 x 64 tiles; one step of the sum (k <= 128), two, three and more; ragged ends
 CASES = [(8192, 256, 2048), (8192, 100, 2048), (8192, 1000, 2000), (8064, 256, 1536), (8000, 60, 1530), (8192, 512, 1536), (8190, 128, 1500),
          (4096, 384, 1536), (4001, 700, 1531), (4096, 256, 1536), (900, 120, 900),
-         (8200, 2048, 1500), (4000, 1300, 4000), (5400, 300, 1500), (8100, 300, 1500)]
+         (8200, 2048, 1500), (4000, 1300, 4000), (5400, 300, 1500), (8100, 300, 1500),
+         # 64 x 64 tiles of long sums, four steps in LDS, and the kernel for few rows at more than its rows: 16, 32 and 64 a workgroup
+         (1000, 4100, 400), (333, 2000, 1001), (900, 1025, 900), (100, 3000, 100), (500, 200, 77), (1500, 300, 20), (40, 4096, 2000),
+         (500, 2048, 500), (200, 4090, 1000), (64, 4096, 9000), (33, 700, 33)]
 
 
 @pytest.mark.parametrize("out", ["bfloat16", "float32"])
