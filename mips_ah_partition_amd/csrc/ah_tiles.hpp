@@ -205,6 +205,12 @@ __device__ __forceinline__ v4i load_chunk(const char* src, int64_t valid, int64_
 __device__ __forceinline__ uint32_t bf16_bits(float f) {  // round to nearest even; NaN stays NaN
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
 }
+// Two of them, in one instruction where the scalar ones take two and three to join them.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
 // One wave's 32 NQ x 32 NP results to memory; sc holds the int8 scales of the tile (its 64 NP columns'
 // scales, their biases, its 64 NQ rows' steps).  The matrix instruction leaves four columns of a
 // row in a lane, 16 rows in a wave.
@@ -304,7 +310,7 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
                 for (int u = 0; u < Y; ++u) value(x, y + u, sx, v + 4 * u);
                 uint32_t w[N / 2];
 #pragma unroll
-                for (int e = 0; e < N / 2; ++e) w[e] = bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16;
+                for (int e = 0; e < N / 2; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
                 const int32_t left = whole ? N : (int32_t)a.J - (j0 + c0 + g * N + y * 16);
                 if (row < 0) {
                 } else if (left >= N) {
@@ -360,7 +366,7 @@ template <int N>
 __device__ __forceinline__ void put_bf16(char* o, const float* v, int32_t left) {
     uint32_t w[N / 2];
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) w[e] = bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16;
+    for (int e = 0; e < N / 2; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
     if (left >= N)
         __builtin_memcpy(o, w, 2 * N);
     else if (left > 0)
@@ -427,7 +433,7 @@ template <int N>
 __device__ __forceinline__ void put_masked(char* o, const float* v, const uint32_t* m, int32_t left, int32_t bypass) {
     uint32_t w[4] = {};
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) w[e] = (bf16_bits(v[2 * e]) | bf16_bits(v[2 * e + 1]) << 16) & m[e];
+    for (int e = 0; e < N / 2; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]) & m[e];
     const v4i x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
     if (left >= N) {
         if constexpr (N == 8)
@@ -474,6 +480,9 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
         const int32_t row = __shfl(x < 4 ? out_row[0] : out_row[1], (x & 3) * 16 + li, 64);
         v4f t[2 * NP];
         take_row(acc, x, t);
+        char* const out = static_cast<char*>(a.out) + ((int64_t)row * a.J + jw) * OB;
+        char* const pre = a.pre + ((int64_t)row * 2 * a.J + jw) * 2;
+        char* const pre_up = pre + a.J * 2;
 #pragma unroll
         for (int y = 0; y < NP; y += Y) {
             const int32_t j = jw + y * 16, left = WHOLE ? N : (int32_t)a.J - j;
@@ -488,22 +497,20 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
             }
             if (row >= 0 && left > 0) {
                 if constexpr (OB == 2) {
-                    put_masked<N>(static_cast<char*>(a.out) + (row * a.J + j) * 2, h, m, left, a.bypass);
+                    put_masked<N>(out + y * 32, h, m, left, a.bypass);
                 } else {
                     v4i w;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         w[e] = m[e >> 1] >> (e & 1 ? 16 : 0) & 1 ? __builtin_bit_cast(int, h[e]) : 0;
-                    char* const o = static_cast<char*>(a.out) + (row * a.J + j) * 4;
                     if (left >= 4)
-                        __builtin_memcpy(o, &w, 16);
+                        __builtin_memcpy(out + y * 64, &w, 16);
                     else
-                        store_left<4>(o, w, left);
+                        store_left<4>(out + y * 64, w, left);
                 }
                 if (a.pre) {
-                    char* const o = a.pre + ((int64_t)row * 2 * a.J + j) * 2;
-                    put_masked<N>(o, u, all, left, a.bypass);
-                    put_masked<N>(o + a.J * 2, v, all, left, a.bypass);
+                    put_masked<N>(pre + y * 32, u, all, left, a.bypass);
+                    put_masked<N>(pre_up + y * 32, v, all, left, a.bypass);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -559,6 +566,9 @@ __device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ]
         if (x + 1 < FQ) ask(x + 1);
         v4f t[2 * NP];
         take_row(acc, x, t);
+        char* const gate = static_cast<char*>(a.out) + ((int64_t)row * 2 * a.J + jw) * 2;
+        char* const up_to = gate + a.J * 2;
+        char* const hidden = a.hidden + ((int64_t)row * a.J + jw) * 2;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int z = 0; z < NP; ++z) {
@@ -578,10 +588,9 @@ __device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ]
                 h[e] = f * up * a.drop.factor;
             }
             if (left > 0) {
-                char* const o = static_cast<char*>(a.out) + ((int64_t)row * 2 * a.J + j) * 2;
-                put_masked<N>(o, da, m, WHOLE ? N : left, a.bypass);
-                put_masked<N>(o + a.J * 2, db, m, WHOLE ? N : left, a.bypass);
-                if (a.hidden) put_masked<N>(a.hidden + (row * a.J + j) * 2, h, m, WHOLE ? N : left, a.bypass);
+                put_masked<N>(gate + z * 64, da, m, WHOLE ? N : left, a.bypass);
+                put_masked<N>(up_to + z * 64, db, m, WHOLE ? N : left, a.bypass);
+                if (a.hidden) put_masked<N>(hidden + z * 64, h, m, WHOLE ? N : left, a.bypass);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -1491,7 +1500,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                 store_left<4>(reinterpret_cast<char*>(o), __builtin_bit_cast(v4i, v), (int32_t)a.J - j);
         } else {
             uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.J + j;
-            const uint32_t w[2] = {bf16_bits(v[0]) | bf16_bits(v[1]) << 16, bf16_bits(v[2]) | bf16_bits(v[3]) << 16};
+            const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
             if (j + 4 <= a.J)
                 __builtin_memcpy(o, w, 8);
             else if (j < a.J)
