@@ -461,9 +461,9 @@ __device__ __forceinline__ void take_row(v4f (&acc)[FQ][FP], int x, v4f (&t)[FP]
         }
 }
 
-// Gated product, 16,384 rows of 16 leaves, 1536 -> 2 x 4096 (412 GFLOP), dropout, both projections kept: 541-575 us at 4 x 4.
+// Gated product, 16,384 rows of 16 leaves, 1536 -> 2 x 4096 (412 GFLOP), dropout, both projections kept: 538-558 us at 4 x 4.
 // The contraction takes 380 of them (without its loads 285; a dense library product of the size 380); what no matrix
-// instruction covers are the stores (402 MB, all CUs at once: 77, 5.2 TB/s), the activation and its rounding (73) and Philox
+// instruction covers are the stores (402 MB, all CUs at once: 77, 5.2 TB/s), the activation and its rounding (60) and Philox
 // (46).  Matrix instructions run in 0.36 of the clocks, at 2.0 GHz.
 // A wave's part of a gated product: a lane holds gate and up of the same columns, in fragments NP apart.  The
 // activation is a template's, chosen once a tile: chosen for each element the compiler computes all and selects.  WHOLE:
@@ -528,7 +528,7 @@ __device__ __forceinline__ void eight_columns(v4f f0, v4f f1, float* v) {
         v[4 + e] = __uint_as_float(t[1]);
     }
 }
-// Gated gradient, 16,384 rows of 16 leaves, 1536 -> 4096 (206 GFLOP, 922 MB), dropout, hidden values too: 370-390 us at 3 x 4,
+// Gated gradient, 16,384 rows of 16 leaves, 1536 -> 4096 (206 GFLOP, 922 MB), dropout, hidden values too: 369-379 us at 3 x 4,
 // the contraction 172 of them (without its loads 140), stores 80 (402 MB), the reads of the projections 35, Philox 27, the
 // rest is the activation, its derivative and their rounding: one after another on every CU, matrix instructions in 0.25 of
 // the clocks.  4 x 4 would not leave registers for a fragment row's projections on their way.
