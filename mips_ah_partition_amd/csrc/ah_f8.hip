@@ -184,13 +184,14 @@ __global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int
     }
 }
 
-// Few rows: one pass over the weights.  A workgroup has 16 columns and 16 FR rows; its eight waves share out the steps
+// Few rows or few columns (few_fragments): few rows are one pass over the weights.  A workgroup has 16 columns and 16 FR rows; its eight waves share out the steps
 // of 128, load both operands from memory into the matrix instruction's layout (lane 16 g + i: bytes 16 g .. and 64 + 16 g ..
 // of row i) and add up through LDS in a fixed order.  XB = 2 or 4: the rows are of that many bytes an element, and every
 // workgroup turns them to codes for itself (a block's largest value lies in four lanes of the wave that needs it, so
 // nothing waits): one launch instead of two.  One row, 1536 -> 4096: 6.0-6.5 us on the GPU, a launch and the chain of
 // loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a launch to quantise.  Up to 16 rows: of
-// 37 x 1001 it took 12.4 us on the GPU, quantising and product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are aligned and 16 elements inside the row or outside together.
+// 37 x 1001 it took 12.4 us on the GPU, quantising and product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are
+// aligned and 16 elements inside the row or outside together.
 template <int XT, int WT, int FR, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int64_t k, bool whole) {
     constexpr int U = FR == 4 ? 2 : 4, MODE = kF8 + XT + 2 * WT;

@@ -1104,7 +1104,8 @@ __global__ __launch_bounds__(kNT, NQ * NP > 4 ? 1 : 2) void prod_tile_kernel(Pro
     // float8: half-step kk multiplies half of the row fragments with all column fragments; the first reads the other half,
     // the second, once a column fragment is done with, the next step's, and the first row fragments.  Between two matrix
     // instructions (32 clocks) stands one load or one fragment's reads: in a lump behind every fourth they cost the
-    // pipe (8192 x 4096 x 16384, quantising included: 627 us, spread 547).  So that a load is three instructions its address is a uniform one
+    // pipe (8192 x 4096 x 16384, quantising included: 627 us, spread 547).  So that a load is three instructions its address is
+    // a uniform one
     // and a lane's offset, the same all along a tile.  That product alone takes 445-515 us (2.1-2.5 PFLOP/s), matrix
     // instructions in 0.54 of the clocks at 1.9-2.0 GHz; without the stores, or without the loads, 60 less.
     auto load8_chunk = [&](int u, int c, uint32_t buf) {
