@@ -540,8 +540,8 @@ int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int
  *   dpre_out bf16 [slots][2n]; may be pre itself;  hidden_out bf16 [slots][n] or NULL.  Rows of no leaf are zero.
  * With these the remaining gradients are the products': dx = ah_grouped_matmul_dx(dpre, W) (n there = 2n here),
  * dW = ah_grouped_matmul_dw(dpre, x), dW_out = ah_grouped_matmul_dw(dy, hidden).
- * Sums are float32 in a fixed order.  relu has the derivative 0 at 0.  A dropped element is 0 whatever it was (a
- * NaN or an infinity too), and so are its gradients.
+ * Sums are float32 in a fixed order.  relu has the derivative 0 at 0, and every activation a NaN's at a NaN.  A dropped
+ * element is 0 whatever it was (a NaN or an infinity too), and so are its gradients.
  * Errors: those of ah_grouped_matmul; AH_ERR_SHAPE (drop outside [0, 1)), AH_ERR_UNSUPPORTED (act, n >
  * AH_MAX_WIDTH / 2, step not 8-byte aligned), AH_ERR_NULL (offsets NULL with L > 1).
  */

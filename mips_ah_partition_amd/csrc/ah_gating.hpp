@@ -33,7 +33,7 @@ __device__ __forceinline__ void activate_grad(int act, float a, float* f, float*
         *df = c + 0.39894228040143268f * a * __builtin_amdgcn_exp2f(-0.72134752044448170f * a * a);
     } else {
         *f = a < 0.0f ? 0.0f : a;
-        *df = a > 0.0f ? 1.0f : 0.0f;
+        *df = a > 0.0f ? 1.0f : a <= 0.0f ? 0.0f : a;
     }
 }
 
