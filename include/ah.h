@@ -594,12 +594,13 @@ int ah_f8_linear(const void* x, int32_t x_dtype, int64_t m, int64_t k, int64_t x
 /* ---------------------------------------------------------------------------
  * Dropout with a mask that is computed and never stored:
  *   out = keep * x / (1 - p') (+ residual)
- * keep[r][c] = (u >= t), t = rint(65536 p), p' = t / 65536, with u the c % 8-th 16 bits (low halves first) of
+ * keep[r][c] = (u >= t), t = min(rint(65536 p), 65535), p' = t / 65536, with u the c % 8-th 16 bits (low halves first) of
  * Philox4x32-10 at the key seed and the counter (c / 8, r, step): a function of seed, step, row and column alone.
  * The gradient is the same call on the output's gradient, without the residual.
  *   x, residual (or NULL), out: rows of n elements of dtype, their strides apart; out may be x or residual
  *   p in [0, 1);  step int64 on the device (read when the kernel runs: a captured graph gets new masks by
  *   counting it up), or NULL = 0
+ * p' is within 2^-17 of p, and within 2^-16 above p = 1 - 2^-17: no p below 1 drops everything.
  * A dropped element is 0 whatever it was.  Float32 arithmetic, rounded once.
  * Errors: AH_ERR_SHAPE (rows < 0, n < 1, a stride < n, p outside [0, 1)), AH_ERR_UNSUPPORTED (dtype, rows or n >=
  * 2^31, step not 8-byte aligned), AH_ERR_NULL.

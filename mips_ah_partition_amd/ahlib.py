@@ -1066,8 +1066,8 @@ def ah_f8_linear(x, w8, w_scale, bias=None, x_type=torch.float8_e4m3fn, out_dtyp
 
 def ah_dropout(x, p, seed, step=None, residual=None, out=None, stream=None):
     """x with each element dropped with probability p and the others multiplied by 1 / (1 - p) (+ residual): float32 or
-    bfloat16 [rows, n].  The mask is a function of seed, step (int64 on the device, none: 0), row and column;
-    the gradient is the same call on the output's gradient."""
+    bfloat16 [rows, n]; p in [0, 1), taken as min(rint(65536 p), 65535) / 65536.  The mask is a function of seed, step
+    (int64 on the device, none: 0), row and column; the gradient is the same call on the output's gradient."""
     x, xs = _rows(x, None, "x")
     dt = _float_code(x.dtype, "x")
     rows, n = x.shape

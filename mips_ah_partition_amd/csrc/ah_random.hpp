@@ -1,10 +1,11 @@
 // Dropout's random numbers: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as
 // 1, 2, 3", 2011), a function of a key and a counter, so that a mask is computed wherever it is needed and
 // never stored.  Key: the caller's seed.  Counter: (column / 8, row, step).  A call gives 128 bits, 16 for each
-// of eight columns; an element stays where its bits are at least t = rint(65536 p), so it is dropped with
+// of eight columns; an element stays where its bits are at least t = min(rint(65536 p), 65535), so it is dropped with
 // the probability t / 2^16, and those that stay are multiplied by 2^16 / (2^16 - t): unbiased for the p that
-// is used, which is off from the given one by 2^-17 at most.  16 bits and not 32: half the generator's work, of
-// which each round is two 32 x 32 -> 64 bit products.
+// is used, which is off from the given one by 2^-17 at most (above 1 - 2^-17, where t = 2^16 would leave nothing and
+// an infinite factor, by less than 2^-16).  16 bits and not 32: half the generator's work, of which each round is
+// two 32 x 32 -> 64 bit products.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
