@@ -303,7 +303,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int6
             else
                 store_left<4>(o, w, some);
         } else {
-            put_bf16<4>(static_cast<char*>(a.out) + (row * a.J + j) * 2, y, some);
+            put_bf16(static_cast<char*>(a.out) + (row * a.J + j) * 2, y, some);
         }
     }
 }

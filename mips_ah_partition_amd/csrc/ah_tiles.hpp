@@ -71,7 +71,7 @@ struct ProdArgs {
     int64_t red;           // summed elements (dw: unused, the leaf's rows)
     void* out;
     int32_t out_f32;
-    int32_t bypass;        // rows of whole 64-byte sectors
+    int32_t bypass;        // rows of whole 64-byte sectors (gated products have stores of their own)
     const float *sx, *sw, *bias;  // int8 (bias: float8 too)
     int32_t act;           // gated: activation, dropout, the projections [slots][2 J] (gate: written, or NULL; grad: read)
     Dropout drop;          // and h (grad; or NULL)
@@ -361,16 +361,13 @@ __device__ __forceinline__ void store_part(const ProdArgs& a, typename Acc<MODE>
     }
 }
 
-// N consecutive bfloat16 values (N of 4 or 8), of which `left` exist.
-template <int N>
+// Four consecutive bfloat16 values, of which `left` exist.
 __device__ __forceinline__ void put_bf16(char* o, const float* v, int32_t left) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]);
-    if (left >= N)
-        __builtin_memcpy(o, w, 2 * N);
+    const uint32_t w[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    if (left >= 4)
+        __builtin_memcpy(o, w, 8);
     else if (left > 0)
-        store_left<2>(o, v4i{(int)w[0], (int)w[1], (int)w[N / 2 - 2], (int)w[N / 2 - 1]}, left);
+        store_left<2>(o, v4i{(int)w[0], (int)w[1], 0, 0}, left);
 }
 // Eight, as they lie in memory (zeros for those that do not exist).
 __device__ __forceinline__ v4i get_bf16x8(const char* p, int32_t left) {
@@ -390,18 +387,17 @@ __device__ __forceinline__ v4i get_bf16x8(const char* p, int32_t left) {
 __device__ __forceinline__ float bf16_at(v4i r, int e) {
     return __uint_as_float(e & 1 ? (uint32_t)r[e >> 1] & 0xFFFF0000u : (uint32_t)r[e >> 1] << 16);
 }
-// Factors of N (4 or 8) columns from j on (a multiple of N) of a row.
-template <int N>
+// Factors of four columns from j on (a multiple of 4) of a row.
 __device__ __forceinline__ void dropout_factors(const Dropout& d, uint64_t step, int32_t row, int32_t j, float* f) {
     if (d.t == 0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) f[e] = 1.0f;
+        for (int e = 0; e < 4; ++e) f[e] = 1.0f;
         return;
     }
     const Philox u = philox(d, step, (uint32_t)row, (uint32_t)j >> 3);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const uint32_t n = N == 4 && (j & 4) ? u.at(e + 4) : u.at(e);
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t n = j & 4 ? u.at(e + 4) : u.at(e);
         f[e] = n >= d.t ? d.factor : 0.0f;
     }
 }
@@ -430,19 +426,14 @@ __device__ __forceinline__ void keep_masks(const Dropout& d, uint64_t step, int3
 }
 // N values as bfloat16 under their masks, of which `left` exist.
 template <int N>
-__device__ __forceinline__ void put_masked(char* o, const float* v, const uint32_t* m, int32_t left, int32_t bypass) {
+__device__ __forceinline__ void put_masked(char* o, const float* v, const uint32_t* m, int32_t left) {
     uint32_t w[4] = {};
 #pragma unroll
     for (int e = 0; e < N / 2; ++e) w[e] = bf16_pair(v[2 * e], v[2 * e + 1]) & m[e];
-    const v4i x = {(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-    if (left >= N) {
-        if constexpr (N == 8)
-            store16(o, x, bypass);
-        else
-            __builtin_memcpy(o, w, 2 * N);
-    } else if (left > 0) {
-        store_left<2>(o, x, left);
-    }
+    if (left >= N)
+        __builtin_memcpy(o, w, 2 * N);
+    else if (left > 0)
+        store_left<2>(o, v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]}, left);
 }
 // Fragment row x of the sums.  A switch over a run-time x, so that what follows stands in the code once and not for every
 // x: unrolled the gated epilogues would outgrow the instruction cache.
@@ -497,7 +488,7 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
             }
             if (row >= 0 && left > 0) {
                 if constexpr (OB == 2) {
-                    put_masked<N>(out + y * 32, h, m, left, a.bypass);
+                    put_masked<N>(out + y * 32, h, m, left);
                 } else {
                     v4i w;
 #pragma unroll
@@ -509,8 +500,8 @@ __device__ __forceinline__ void store_gate(const ProdArgs& a, v4f (&acc)[2 * NQ]
                         store_left<4>(out + y * 64, w, left);
                 }
                 if (a.pre) {
-                    put_masked<N>(pre + y * 32, u, all, left, a.bypass);
-                    put_masked<N>(pre_up + y * 32, v, all, left, a.bypass);
+                    put_masked<N>(pre + y * 32, u, all, left);
+                    put_masked<N>(pre_up + y * 32, v, all, left);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -588,9 +579,9 @@ __device__ __forceinline__ void store_grad(const ProdArgs& a, v4f (&acc)[2 * NQ]
                 h[e] = f * up * a.drop.factor;
             }
             if (left > 0) {
-                put_masked<N>(gate + z * 64, da, m, WHOLE ? N : left, a.bypass);
-                put_masked<N>(up_to + z * 64, db, m, WHOLE ? N : left, a.bypass);
-                if (a.hidden) put_masked<N>(hidden + z * 64, h, m, WHOLE ? N : left, a.bypass);
+                put_masked<N>(gate + z * 64, da, m, WHOLE ? N : left);
+                put_masked<N>(up_to + z * 64, db, m, WHOLE ? N : left);
+                if (a.hidden) put_masked<N>(hidden + z * 64, h, m, WHOLE ? N : left);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -1527,8 +1518,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
             if (MODE == kGate && a.pre) {
                 const float none[4] = {};
                 char* const p = a.pre + ((int64_t)row * 2 * a.J + c) * 2;
-                put_bf16<4>(p, none, left);
-                put_bf16<4>(p + a.J * 2, none, left);
+                put_bf16(p, none, left);
+                put_bf16(p + a.J * 2, none, left);
             }
         }
         return;
@@ -1683,14 +1674,14 @@ __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {
                 } else if constexpr (G == 2) {
                     const v4f up = sum_of(FR + f);
                     float drop[4];
-                    dropout_factors<4>(a.drop, call_step, out_row[f], j, drop);
+                    dropout_factors(a.drop, call_step, out_row[f], j, drop);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = dropped(activate(a.act, t[e]) * up[e], drop[e]);
                     if (a.pre) {
                         const float gates[4] = {t[0], t[1], t[2], t[3]}, ups[4] = {up[0], up[1], up[2], up[3]};
                         char* const p = a.pre + ((int64_t)out_row[f] * 2 * a.J + j) * 2;
-                        put_bf16<4>(p, gates, (int32_t)a.J - j);
-                        put_bf16<4>(p + a.J * 2, ups, (int32_t)a.J - j);
+                        put_bf16(p, gates, (int32_t)a.J - j);
+                        put_bf16(p + a.J * 2, ups, (int32_t)a.J - j);
                     }
                 } else {
                     v = t;
@@ -1876,9 +1867,7 @@ hipError_t launch_prod(ProdArgs a, int32_t fan, hipStream_t stream) {
     a.fan_shift = 31 + l;
     a.fan_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + fan - 1) / fan);
     const int64_t pitch = a.J * (a.out_f32 ? 4 : 2);
-    uintptr_t sectors = reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch;
-    if (is_gated(MODE)) sectors |= reinterpret_cast<uintptr_t>(a.pre) | reinterpret_cast<uintptr_t>(a.hidden);
-    a.bypass = MODE != kFwd && !is_gated(MODE) && (sectors & 63) == 0;
+    a.bypass = MODE != kFwd && !is_gated(MODE) && ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)pitch) & 63) == 0;
     if constexpr (MODE == kI8 || MODE == kFwd || MODE == kGate) {
         switch (row_fragments<MODE>(a)) {
             case 1: return launch_rows<MODE, 1>(a, whole, stream);
