@@ -11,3 +11,14 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (runs through the C-ABI library)")
     config.addinivalue_line("markers", "slow: long CPU test")
+
+
+# Their reference for QueryHead.step's gradient of the features leaves out the path through the gates
+# (d gate_f / d x; at 900 rows central differences of the forward pass along a random direction give -0.11384, the step -0.11384,
+# the reference -0.02831); test_gpu_head_training.py holds the whole gradient.  They run last, so that a run that stops at
+# its first failure has run everything else.
+HELD_GATES = tuple(f"test_gpu_query_head.py::test_forward_and_gradients[{m}]" for m in (50, 900))
+
+
+def pytest_collection_modifyitems(items):
+    items.sort(key=lambda item: item.nodeid.endswith(HELD_GATES))
