@@ -532,12 +532,14 @@ int ah_distill_topk(const void* logits, int32_t dtype, int64_t n, int64_t V, int
  *   drop, seed, step: dropout of h as in ah_dropout, row = slot, column in [0, n); drop 0: none
  *   pre_out bf16 [slots][2n] the two projections (gate, up), or NULL: what the backward pass needs
  *   out [slots][n] of out_dtype: h.  Rows of no leaf are zero in both.
- * h is computed from the float32 sums and rounded once; pre_out is rounded to bf16.
+ * h is computed from the float32 sums and rounded once; pre_out is rounded to bf16.  The activation is within (|a| + 16)
+ * 2^-23 (silu; 0 from about -87 down, where e^-a leaves float32) or (a^2 + 20) 2^-23 (gelu) of its value.
  * ah_grouped_gated_grad: from the gradient of y to those of the projections, in one kernel.  With dh = W_out^T dy
  * (float32, not stored), a and b from pre, keep and p' as in the forward call:
- *   dpre_out[s] = (dh b act'(a), dh act(a)) keep / (1 - p'),   hidden_out[s] = h
+ *   dpre_out[s] = (dh b act'(a), dh act(a)) keep / (1 - p'),   hidden_out[s] = keep act(a) b / (1 - p')
  *   dy  bf16 [slots] rows of d, dy_stride apart;  w bf16 [L][d][n] (W_out);  pre bf16 [slots][2n]
- *   dpre_out bf16 [slots][2n]; may be pre itself;  hidden_out bf16 [slots][n] or NULL.  Rows of no leaf are zero.
+ *   dpre_out bf16 [slots][2n]; may be pre itself;  hidden_out bf16 [slots][n] or NULL: h again, from the bfloat16
+ *   projections, so a rounding of theirs away from the forward call's.  Rows of no leaf are zero.
  * With these the remaining gradients are the products': dx = ah_grouped_matmul_dx(dpre, W) (n there = 2n here),
  * dW = ah_grouped_matmul_dw(dpre, x), dW_out = ah_grouped_matmul_dw(dy, hidden).
  * Sums are float32 in a fixed order.  relu has the derivative 0 at 0, and every activation a NaN's at a NaN.  A dropped

@@ -946,7 +946,7 @@ def ah_grouped_gated_grad(dy, w, pre, offsets=None, order=None, act="silu", drop
                           want_hidden=True, dpre_out=None, hidden_out=None, stream=None):
     """From the gradient of a gated block's output to its projections': dy bfloat16 [slots, d], w bfloat16 [L, d, n] (the
     output layer), pre bfloat16 [slots, 2n] and the dropout's arguments as in the forward call.  Returns (dpre bfloat16
-    [slots, 2n], h bfloat16 [slots, n] computed again for the output layer's gradient, or None)."""
+    [slots, 2n], h bfloat16 [slots, n] computed again from pre for the output layer's gradient, or None)."""
     dy, dys = _rows(dy, torch.bfloat16, "dy")
     _is(w, torch.bfloat16, "w", 3)
     _is(pre, torch.bfloat16, "pre", 2)

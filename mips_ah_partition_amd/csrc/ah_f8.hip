@@ -184,14 +184,14 @@ __global__ __launch_bounds__(kColThreads) void f8_columns_kernel(const T* x, int
     }
 }
 
-// Few rows or few columns (few_fragments): few rows are one pass over the weights.  A workgroup has 16 columns and 16 FR rows; its eight waves share out the steps
-// of 128, load both operands from memory into the matrix instruction's layout (lane 16 g + i: bytes 16 g .. and 64 + 16 g ..
-// of row i) and add up through LDS in a fixed order.  XB = 2 or 4: the rows are of that many bytes an element, and every
-// workgroup turns them to codes for itself (a block's largest value lies in four lanes of the wave that needs it, so
-// nothing waits): one launch instead of two.  One row, 1536 -> 4096: 6.0-6.5 us on the GPU, a launch and the chain of
-// loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a launch to quantise.  Up to 16 rows: of
-// 37 x 1001 it took 12.4 us on the GPU, quantising and product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are
-// aligned and 16 elements inside the row or outside together.
+// Few rows or few columns (few_fragments): few rows are one pass over the weights.  A workgroup has 16 columns and 16 FR
+// rows; its eight waves share out the steps of 128, load both operands from memory into the matrix instruction's layout
+// (lane 16 g + i: bytes 16 g .. and 64 + 16 g .. of row i) and add up through LDS in a fixed order.  XB = 2 or 4: the rows
+// are of that many bytes an element, and every workgroup turns them to codes for itself (a block's largest value lies in
+// four lanes of the wave that needs it, so nothing waits): one launch instead of two.  One row, 1536 -> 4096: 6.0-6.5 us
+// on the GPU, a launch and the chain of loads, codes, sum and exchange (6.4 MB of weights are 1.2); a call 10.0, 12.1 with a
+// launch to quantise.  Up to 16 rows (kFewRows, with its figures): of 37 x 1001 it took 12.4 us on the GPU, quantising and
+// product in turn 3.2 + 5.4.  whole: their chunks of 16 bytes are aligned and 16 elements inside the row or outside together.
 template <int XT, int WT, int FR, int XB>
 __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int64_t k, bool whole) {
     constexpr int U = FR == 4 ? 2 : 4, MODE = kF8 + XT + 2 * WT;
@@ -277,7 +277,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void f8_few_kernel(ProdArgs a, int6
                     }
                 }
 #pragma unroll
-                for (int f = 0; f < FR; ++f) acc[f] = mma8<MODE>(halves(pv[u][0], pv[u][1]), halves(qv[u][f][0], qv[u][f][1]), acc[f], sp[u], sq[u][f]);
+                for (int f = 0; f < FR; ++f)
+                    acc[f] = mma8<MODE>(halves(pv[u][0], pv[u][1]), halves(qv[u][f][0], qv[u][f][1]), acc[f], sp[u], sq[u][f]);
             }
     }
 #pragma unroll
@@ -352,10 +353,12 @@ int few_fragments(const ProdArgs& a, double tiles) {
     } few[] = {{1, 0.9, 420, 7.0}, {2, 1.4, 200, 5.5}, {4, 2.3, 60, 7.0}};
     int best = 0;
     for (const auto& f : few) {
-        const int64_t rows = (a.T + 16 * f.fr - 1) / (16 * f.fr), wgs = rows * ((a.J + 15) / 16), steps = (a.red + 127) / 128;
+        const int64_t rows = (a.T + 16 * f.fr - 1) / (16 * f.fr), wgs = rows * ((a.J + 15) / 16),
+                      steps = (a.red + 127) / 128;
         const double start = (double)((steps + kRowWaves - 1) / kRowWaves) * f.chain +
                              (wgs > kCUs ? (double)(wgs - kCUs) / f.starts : 0.0),
-                     read = (double)wgs * 16 * (1 + f.fr) * (double)a.red * 1e-6 / f.rate, time = 2.0 + (start > read ? start : read);
+                     read = (double)wgs * 16 * (1 + f.fr) * (double)a.red * 1e-6 / f.rate,
+                     time = 2.0 + (start > read ? start : read);
         if (rows <= 65535 && time < tiles) {  // (a launch's second dimension)
             best = f.fr;
             tiles = time;
@@ -423,6 +426,11 @@ hipError_t launch_f8_matmul(const F8Problem& g, const float* bias, void* out, in
 }
 
 // Workspace: the rows' codes, then their scale bytes; none for rows that the product turns to codes itself.
+// Measured, us, codes in the product | in a launch of their own (2, 8 and 16 rows; on the GPU, then a call):
+//   1536 -> 4096    5.7  6.0  6.4 | 5.7  6.0  6.4      9.5  9.5  9.5 | 18.7 18.8 18.8
+//   4096 -> 16384   38.6 40.5 43.6 | 17.2 18.5 20.7    37.9 40.3 43.1 | 18.7 18.6 20.5
+// One fragment of rows is what every workgroup can keep; wide layers, where each of many workgroups makes the same codes again,
+// would be faster by two launches, which the rule does not tell apart.
 constexpr int64_t kFewRows = 16;
 static size_t f8_code_bytes(int64_t m, int64_t k) { return (size_t)m * ((k + kBlk - 1) / kBlk * kBlk); }
 size_t f8_linear_workspace_bytes(int64_t m, int64_t k) {

@@ -1465,8 +1465,9 @@ __device__ __forceinline__ float step_of(float m) { return m < INFINITY ? m / 12
 // latency (7.0 on the GPU; 15.6 with tiles and quantising in a launch of its own).
 constexpr int kRowWaves = 8;
 // STRIP (gated sums of at most 512 bytes, eight pieces): nothing to share out, so every wave has 16 columns of its own and the
-// whole sum (999 slots of 37 leaves, 100 -> 2 x 385, on the GPU: 12.4 us, 18 with the sum shared by eight waves).  Bound
-// by the chain of leaf starts, order, row and weights, each a load that waits for the one before.  One token, 1536 ->
+// whole sum (999 slots of 37 leaves, 100 -> 2 x 385, on the GPU: 12.1 us, 18 with the sum shared by eight waves).  Bound
+// by the chain of leaf starts, order, row and weights, each a load that waits for the one before, and by the epilogue
+// (with silu in gelu's place 9.8; a Philox call makes eight numbers of which a lane uses four).  One token, 1536 ->
 // 2 x 4096, shares the sum: 7.5 us, of which 25 MB of weights are 4.7.
 template <int MODE, int FR, bool WHOLE, int XB, bool STRIP = false>
 __global__ __launch_bounds__(kRowWaves * 64) void prod_rows_kernel(ProdArgs a) {

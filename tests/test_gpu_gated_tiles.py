@@ -1,6 +1,5 @@
-"""The large tile shapes of the gated products (256 x 256, 192 x 256), which only batches of thousands of rows reach: their ring
-of half-steps, and dropout's numbers made in the loop where the sum has many steps and behind it where it has few.  References and
-tolerances as in test_gpu_gated.
+"""Gated products of thousands of rows: the large tile shapes (256 x 256, 192 x 256) with their ring of half-steps where the sum
+is long enough, 128 x 128 where it is not, and rows of no leaf.  References and tolerances as in test_gpu_gated.
 """
 import pytest
 
