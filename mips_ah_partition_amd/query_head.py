@@ -105,6 +105,8 @@ class QueryHead:
         features without it.  want_dx="hidden" (8-bit float trunk): the gradient of the hidden states, bfloat16 [m, h],
         in its place; trunk_lr: the trunk's own rate.  Both are products of 8-bit codes like the trunk's, whose
         roundings count as the identity."""
+        if isinstance(want_dx, str) and want_dx != "hidden":
+            raise ValueError(f'want_dx must be a truth value or "hidden", got {want_dx!r}')
         if self.trunk_type != "f8" and (want_dx == "hidden" or trunk_lr):
             raise ValueError("only an 8-bit float trunk has gradients")
         m = hidden.shape[0]
