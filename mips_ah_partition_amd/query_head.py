@@ -24,6 +24,8 @@ from . import ahlib
 
 
 class QueryHead:
+    ROWS = ahlib.AH_MAX_WIDTH  # rows that a product of the trunk's gradient sums (a multiple of 128)
+
     def __init__(self, trunk: torch.Tensor, router: torch.Tensor, dim: int, fan: int = 2, seed: int = 0,
                  inner: int = 0, act: str = "silu", drop: float = 0.0, trunk_type: str = "i8"):
         """trunk: float32 [k, h], the linear layer's weights (h: the hidden width); router: float32
@@ -159,16 +161,25 @@ class QueryHead:
 
     def _trunk_back(self, dx, hidden, want_dx, trunk_lr):
         """Gradients through the 8-bit float layer x = W hidden: dx W and dx^T hidden, both sums over blocks of 128 with
-        their own scales (so the transposed operands are quantised along the other side)."""
-        codes, scale, codes_t, scale_t = ahlib.ah_f8_quantize(dx, want_rows=want_dx == "hidden", want_columns=bool(trunk_lr))
-        if want_dx == "hidden":
-            dx = ahlib.ah_f8_matmul(codes, scale, self._codes[2], self._codes[3], out_dtype=torch.bfloat16)
+        their own scales (so the transposed operands are quantised along the other side).  A product sums at most
+        2^20 rows; more are added up in order."""
+        m, dw = dx.shape[0], None
+        back = torch.empty((m, hidden.shape[1]), dtype=torch.bfloat16, device=dx.device) if want_dx == "hidden" else dx
+        for a in range(0, max(m, 1), self.ROWS):
+            part = slice(a, a + self.ROWS)
+            codes, scale, codes_t, scale_t = ahlib.ah_f8_quantize(dx[part], want_rows=want_dx == "hidden",
+                                                                  want_columns=bool(trunk_lr))
+            if want_dx == "hidden":
+                ahlib.ah_f8_matmul(codes, scale, self._codes[2], self._codes[3], out=back[part])
+            if trunk_lr:
+                _, _, h8, hs = ahlib.ah_f8_quantize(hidden[part], want_rows=False, want_columns=True)
+                d = ahlib.ah_f8_matmul(codes_t, scale_t, h8, hs, out_dtype=torch.float32)
+                dw = d if dw is None else dw.add_(d)
         if trunk_lr:
-            _, _, h8, hs = ahlib.ah_f8_quantize(hidden, want_rows=False, want_columns=True)
-            self.trunk.add_(ahlib.ah_f8_matmul(codes_t, scale_t, h8, hs, out_dtype=torch.float32), alpha=-trunk_lr)
+            self.trunk.add_(dw, alpha=-trunk_lr)
             ahlib.ah_f8_quantize(self.trunk, want_columns=True, codes_out=self._codes[0], scale_out=self._codes[1],
                                  codes_t_out=self._codes[2], scale_t_out=self._codes[3])
-        return dx if want_dx else None
+        return back if want_dx else None
 
 
 class Items:
